@@ -416,6 +416,7 @@ def time_graph(graph, reps, stream, barrier=None):
 PROFILES = {
     "decode2": ("decode_b8_ctx32k_fp8_ncu.md",
                 ("paged_quantized_kv_quant_b200/csrc/decode.cu",
+                 "paged_quantized_kv_quant_b200/csrc/decode_split.cuh",
                  "paged_quantized_kv_quant_b200/csrc/common.cuh",
                  "paged_quantized_kv_quant_b200/csrc/quant.cuh",
                  "paged_quantized_kv_quant_b200/csrc/split_map.cuh")),
@@ -423,6 +424,7 @@ PROFILES = {
                 ("paged_quantized_kv_quant_b200/csrc/decode_tc.cu",
                  "paged_quantized_kv_quant_b200/csrc/kv_stage.cuh",
                  "paged_quantized_kv_quant_b200/csrc/decode.cu",
+                 "paged_quantized_kv_quant_b200/csrc/decode_split.cuh",
                  "paged_quantized_kv_quant_b200/csrc/split_map.cuh",
                  "paged_quantized_kv_quant_b200/csrc/common.cuh",
                  "paged_quantized_kv_quant_b200/csrc/tc.cuh")),

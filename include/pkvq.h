@@ -71,7 +71,14 @@ typedef enum {
     /* The fp16 values themselves, no scale (2 bytes per element).  Source:
      * "ReVolta" PyPI page, first section ("KV formats: FP8 E4M3, FP16, and
      * INT8"). */
-    PKVQ_KV_FP16 = 3
+    PKVQ_KV_FP16 = 3,
+    /* INT8 codes with one fp32 scale per (block, KV head) for K and one for V,
+     * made from the tokens as they are written (pkvq_kv_write_block_quant):
+     * no calibration, and 8 bytes of scales per block and head instead of 4
+     * per token and head. */
+    PKVQ_KV_INT8_BLOCK = 4,
+    /* E4M3 codes with the same scales per (block, KV head). */
+    PKVQ_KV_E4M3_BLOCK = 5
 } pkvq_kv_dtype;
 
 /* Describes caller-owned cache memory.  All pointers device, 16-byte aligned. */
@@ -82,7 +89,7 @@ typedef struct {
     int32_t num_kv_heads;
     int32_t head_dim;       /* must be 128 */
     void *k_cache;          /* [num_blocks][num_kv_heads][block_size][head_dim] elements:
-                               1 byte (E4M3, E5M2, INT8) or 2 (FP16) */
+                               1 byte (FP16: 2) */
     void *v_cache;
     const float *k_scale;   /* FP8 formats: fp32 [num_kv_heads] (or [1], see
                                scale_per_layer); INT8, FP16: unused (NULL) */
@@ -92,6 +99,8 @@ typedef struct {
     int32_t scale_per_layer; /* FP8 formats: nonzero = k_scale and v_scale hold one value
                                 each, shared by every KV head ("ReVolta" PyPI page, "E4M3
                                 KV": one calibrated K and V scale per layer) */
+    float *k_scale_blk;     /* block-scaled formats: fp32 [num_blocks][num_kv_heads]; else unused */
+    float *v_scale_blk;
 } pkvq_cache;
 
 /*
@@ -118,6 +127,39 @@ typedef struct {
 PKVQ_API pkvq_status pkvq_kv_write_quant(const pkvq_cache *cache, const void *k, const void *v,
                                 const int32_t *slot_mapping, int32_t num_tokens,
                                 void *stream);
+
+/*
+ * KV write + quantise into a block-scaled cache (PKVQ_KV_INT8_BLOCK,
+ * PKVQ_KV_E4M3_BLOCK).  The n_b = cu[b + 1] - cu[b] new tokens of sequence b are
+ * its positions context_lens[b] - n_b .. context_lens[b] - 1 (positions below 0
+ * are skipped), in the blocks its table row gives them.  With Q = 127 or 448,
+ * for every block they touch, every KV head, K and V each:
+ *   s = RN(A / Q), A the largest |x| of the call's tokens in that block and head
+ *       (+-inf counts, and is stored, as +-65504; NaN as 0);
+ *   if the block holds older tokens (positions below context_lens[b] - n_b):
+ *       s = max(s, stored scale), and where it grew their codes become
+ *       round(RN(value(code) * RN(stored scale / s)));
+ *   code = round(RN(x / s)), clamped to +-Q (s == 0 -> 0); s is stored.
+ * All fp32, division and product rounded to nearest, round() to the nearest
+ * code, ties to even.  The value of a code is code * s.  Rows at or behind
+ * context_lens[b] are left as they were.
+ *   k, v            fp16 [cu[batch]][num_kv_heads][head_dim], 16-byte aligned,
+ *                   sequences packed
+ *   cu_seqlens_new  int32 [batch + 1], cu[0] = 0, nondecreasing; equal entries:
+ *                   the sequence gets nothing
+ *   block_table     int32 [batch][max_blocks_per_seq]
+ *   context_lens    int32 [batch], the new tokens included
+ *   max_new_len     host-side upper bound of n_b (sizes the launch)
+ * A block that receives tokens must belong to one sequence of the call only.
+ * batch == 0 or max_new_len == 0 is a no-op.  Other formats return
+ * PKVQ_ERR_UNSUPPORTED, as pkvq_kv_write_quant does for these two (a token
+ * alone does not say what its block's scale becomes).  Codes and scales are
+ * bit-exact with the definition above.
+ */
+PKVQ_API pkvq_status pkvq_kv_write_block_quant(const pkvq_cache *cache, const void *k, const void *v,
+                                const int32_t *cu_seqlens_new, const int32_t *block_table,
+                                int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                int32_t batch, int32_t max_new_len, void *stream);
 
 /*
  * Workspace bytes pkvq_paged_attn_decode needs for this shape on the
@@ -270,6 +312,77 @@ PKVQ_API pkvq_status pkvq_paged_attn_decode_append(const pkvq_cache *cache, cons
                                    float softmax_scale, const pkvq_attn_opts *opts,
                                    void *workspace, size_t workspace_bytes, void *stream);
 
+/* Workspace bytes of pkvq_paged_attn_decode_weights (0 on invalid arguments):
+ * the split-KV partial states and the fp32 score of every (query row, key). */
+PKVQ_API size_t pkvq_decode_weights_workspace_bytes(int32_t batch, int32_t q_len,
+                                   int32_t num_q_heads, int32_t max_context_len,
+                                   const pkvq_cache *cache);
+
+/*
+ * pkvq_paged_attn_decode_ex that also accumulates how much every key was
+ * attended to, for pkvq_kv_evict.  With s_rj the scaled score and lse_r the
+ * natural-log sum-exp of query row r (query token t of q_len, query head of KV
+ * head h):
+ *   weights[b][h][j] += sum over rows r of e^(s_rj - lse_r), j visible to r.
+ *   weights        fp32 [batch][num_kv_heads][weight_stride], read and
+ *                  written for keys j < context_lens[b] inside the sliding
+ *                  window's blocks; entries of tokens that are new since the last
+ *                  call must hold 0 (or whatever they are to start from)
+ *   weight_stride  elements between rows, at least max_context_len
+ * Sums are fp32 and their order is fixed: the same call gives the same bits.
+ * All other arguments, results and errors as pkvq_paged_attn_decode_ex; the
+ * workspace is sized by pkvq_decode_weights_workspace_bytes.  batch and
+ * num_kv_heads at most 65535.
+ */
+PKVQ_API pkvq_status pkvq_paged_attn_decode_weights(const pkvq_cache *cache, const void *q,
+                                   void *out, float *lse_out, const int32_t *block_table,
+                                   int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                   int32_t batch, int32_t q_len, int32_t num_q_heads,
+                                   int32_t max_context_len, float softmax_scale,
+                                   const pkvq_attn_opts *opts, float *weights,
+                                   int64_t weight_stride, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction by accumulated attention weight: every (sequence, KV head) keeps at
+ * most `budget` of its n = context_lens[b] tokens and moves them, in order, to
+ * new blocks.  If n <= budget all are kept; otherwise positions 0 ..
+ * num_sink - 1, n - num_recent .. n - 1, and those budget - num_sink -
+ * num_recent of the others with the largest weight (equal weights: the lowest
+ * position; NaN ranks lowest).  Heads choose for themselves, so a position of
+ * the new blocks holds different tokens for different heads.  With m = min(n,
+ * budget), for r < m:
+ *   keep_out[b][h][r] = the r-th kept position (ascending); -1 for r >= m
+ *   token keep_out[b][h][r] becomes token r of sequence b in the blocks
+ *   dst_block_table[b] gives; per-token scales move along
+ *   weights_out[b][h][r] = its weight; 0 for r >= m, to the row's end
+ *   new_context_lens[b] = m
+ * Block-scaled formats: a new block's scale is the largest of its tokens' source
+ * scales; codes from a block with a smaller one become
+ * round(RN(value(code) * RN(s_src / s_dst))).
+ *   weights          fp32 [batch][num_kv_heads][weight_stride]; each context
+ *                    length at most weight_stride
+ *   dst_block_table  int32 [batch][dst_max_blocks], dst_max_blocks * block_size
+ *                    >= budget; entries behind a sequence's new length are not
+ *                    read.  Blocks must be distinct and hold no token of the
+ *                    call's sequences; their rows behind the new length are
+ *                    left as they were.  Old blocks are not changed.
+ *   keep_out         int32 [batch][num_kv_heads][budget]
+ *   new_context_lens int32 [batch], not the context_lens array
+ *   weights_out      nullable fp32 [batch][num_kv_heads][weight_out_stride],
+ *                    weight_out_stride >= budget; must not overlap weights
+ * num_sink + num_recent must not exceed budget; batch and num_kv_heads at most
+ * 65535.  batch == 0 is a no-op.
+ */
+PKVQ_API pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights,
+                                   int64_t weight_stride, const int32_t *block_table,
+                                   int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                   int32_t batch, int32_t budget, int32_t num_sink,
+                                   int32_t num_recent, const int32_t *dst_block_table,
+                                   int32_t dst_max_blocks, int32_t *keep_out,
+                                   int32_t *new_context_lens, float *weights_out,
+                                   int64_t weight_out_stride, void *stream);
+
 /*
  * pkvq_paged_attn_prefill with options (sliding window; query_pos must be
  * NULL, else PKVQ_ERR_UNSUPPORTED).
@@ -308,7 +421,8 @@ PKVQ_API pkvq_status pkvq_merge_attn_states(const void *parts_out, const float *
  * unified addressing the host pointer serves as is).  Source: "ReVolta" PyPI
  * page, "KV offload modes" (cached pages kept in CPU memory and brought
  * back).  For i < n, block pairs[2i] of src becomes block pairs[2i + 1] of
- * dst: its K and V elements and, for INT8, its per-token scales.  The
+ * dst: its K and V elements and its scales (INT8: per token; block-scaled
+ * formats: per block and head).  The
  * per-head FP8 scales belong to the cache, not to a block, and are not
  * copied.  pairs: int32 [n][2], device-addressable.  Destination blocks must
  * be distinct and none may be a source block of the same call; ids outside

@@ -8,10 +8,13 @@ kernels; there is no CPU or PyTorch fallback, and loading fails loudly when
 the library has not been built.
 
 Entry points (same names as the C ABI, without the ``pkvq_`` prefix):
-  kv_write_quant, decode_workspace_bytes, paged_attn_decode (with the _ex
-  options as keyword arguments: sliding_window, query_pos),
-  paged_attn_prefill (sliding_window), merge_attn_states, kv_copy_blocks,
-  device_status, status_string, version.  ``dcp`` adds the all-gather step
+  kv_write_quant, kv_write_block_quant (block-scaled formats),
+  decode_workspace_bytes, paged_attn_decode (with the _ex options as keyword
+  arguments: sliding_window, query_pos), paged_attn_decode_append,
+  paged_attn_decode_weights and decode_weights_workspace_bytes (decode that
+  accumulates every key's attention weight), kv_evict (eviction by those
+  weights), paged_attn_prefill (sliding_window), merge_attn_states,
+  kv_copy_blocks, device_status, status_string, version.  ``dcp`` adds the all-gather step
   of sequence-sharded decode (torch.distributed plumbing).
 """
 from __future__ import annotations
@@ -32,10 +35,17 @@ KV_FP8_E4M3 = 0
 KV_INT8 = 1
 KV_FP8_E5M2 = 2
 KV_FP16 = 3
+KV_INT8_BLOCK = 4
+KV_E4M3_BLOCK = 5
+_BLOCK_FORMATS = (KV_INT8_BLOCK, KV_E4M3_BLOCK)
 _FP8_FORMATS = (KV_FP8_E4M3, KV_FP8_E5M2)
 
 EXPORTED = (
     "pkvq_kv_write_quant",
+    "pkvq_kv_write_block_quant",
+    "pkvq_decode_weights_workspace_bytes",
+    "pkvq_paged_attn_decode_weights",
+    "pkvq_kv_evict",
     "pkvq_decode_workspace_bytes",
     "pkvq_paged_attn_decode_append",
     "pkvq_paged_attn_decode",
@@ -80,6 +90,8 @@ class CacheStruct(ctypes.Structure):
         ("k_scale_tok", ctypes.c_void_p),
         ("v_scale_tok", ctypes.c_void_p),
         ("scale_per_layer", ctypes.c_int32),
+        ("k_scale_blk", ctypes.c_void_p),
+        ("v_scale_blk", ctypes.c_void_p),
     ]
 
 
@@ -106,6 +118,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     lib.pkvq_kv_write_quant.restype = I32
     lib.pkvq_kv_write_quant.argtypes = [P, P, P, P, I32, P]
+    lib.pkvq_kv_write_block_quant.restype = I32
+    lib.pkvq_kv_write_block_quant.argtypes = [P, P, P, P, P, I32, P, I32, I32, P]
+    lib.pkvq_decode_weights_workspace_bytes.restype = SZ
+    lib.pkvq_decode_weights_workspace_bytes.argtypes = [I32, I32, I32, I32, P]
+    lib.pkvq_paged_attn_decode_weights.restype = I32
+    lib.pkvq_paged_attn_decode_weights.argtypes = [P, P, P, P, P, I32, P, I32, I32, I32, I32,
+                                                   ctypes.c_float, P, P, ctypes.c_int64, P, SZ,
+                                                   P]
+    lib.pkvq_kv_evict.restype = I32
+    lib.pkvq_kv_evict.argtypes = [P, P, ctypes.c_int64, P, I32, P, I32, I32, I32, I32, P, I32,
+                                  P, P, P, ctypes.c_int64, P]
     lib.pkvq_decode_workspace_bytes.restype = SZ
     lib.pkvq_decode_workspace_bytes.argtypes = [I32, I32, I32, I32, P]
     lib.pkvq_paged_attn_decode.restype = I32
@@ -178,10 +201,46 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream, device=None) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream=None):
+    """Context in which `t`'s device and the call's stream are the current ones:
+    launches go there, and what the call allocates belongs to that stream."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if t.get_device() == torch.cuda.current_device():
+        return _SAME_DEVICE
+    return torch.cuda.device(t.device)
+
+
+def _batch(B: int, q: torch.Tensor, out, lse, block_table, context_lens) -> None:
+    """The shapes that go with a batch of B sequences and the queries q."""
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.shape != q.shape[:-1]:
+        raise ValueError("lse must have q's shape without head_dim")
+    if block_table.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError(f"block_table and context_lens must have {B} rows")
+
+
+def _args(device: int, **tensors) -> None:
+    """Checks (tensor, dtype, shape) triples: dtype, exact shape, contiguous, on
+    CUDA device `device`.  None tensors are skipped."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        _need(t, dtype, name)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}")
 
 
 def _need(t: torch.Tensor, dtype, name: str, ndim: Optional[int] = None,
@@ -204,7 +263,8 @@ class PagedKVCache:
     """Caller-owned paged cache: elements [num_blocks][Hkv][block_size][D x
     elem_bytes] uint8 (E4M3 / E5M2 bits, int8 two's complement, or fp16 bits),
     fp32 scales for the FP8 formats ([Hkv], or [1] with scale_per_layer),
-    per-(block, head, token) fp16 scales for INT8."""
+    per-(block, head, token) fp16 scales for INT8, fp32 scales
+    [num_blocks][Hkv] for the block-scaled formats."""
     dtype: int
     k_cache: torch.Tensor
     v_cache: torch.Tensor
@@ -213,6 +273,8 @@ class PagedKVCache:
     k_scale_tok: Optional[torch.Tensor] = None
     v_scale_tok: Optional[torch.Tensor] = None
     scale_per_layer: bool = False
+    k_scale_blk: Optional[torch.Tensor] = None
+    v_scale_blk: Optional[torch.Tensor] = None
 
     @staticmethod
     def allocate(dtype: int, num_blocks: int, block_size: int, num_kv_heads: int,
@@ -236,6 +298,9 @@ class PagedKVCache:
                                 scale_per_layer=scale_per_layer)
         if dtype == KV_FP16:
             return PagedKVCache(dtype, kc, vc)
+        if dtype in _BLOCK_FORMATS:
+            return PagedKVCache(dtype, kc, vc, k_scale_blk=zeros(shape[:2], torch.float32),
+                                v_scale_blk=zeros(shape[:2], torch.float32))
         kst, vst = zeros(shape[:3], torch.float16), zeros(shape[:3], torch.float16)
         return PagedKVCache(dtype, kc, vc, k_scale_tok=kst, v_scale_tok=vst)
 
@@ -265,6 +330,14 @@ class PagedKVCache:
         elif self.dtype == KV_INT8:
             _need(self.k_scale_tok, torch.float16, "k_scale_tok", 3, host_ok=device_ok)
             _need(self.v_scale_tok, torch.float16, "v_scale_tok", 3, host_ok=device_ok)
+        elif self.dtype in _BLOCK_FORMATS:
+            for name in ("k_scale_blk", "v_scale_blk"):
+                t = getattr(self, name)
+                _need(t, torch.float32, name, 2, host_ok=device_ok)
+                if t.shape != self.k_cache.shape[:2]:
+                    raise ValueError(f"{name} must be [num_blocks][num_kv_heads]")
+            if self.v_cache.shape != self.k_cache.shape:
+                raise ValueError("k_cache and v_cache must have the same shape")
         nb, hkv, bs, rb = self.k_cache.shape
         return CacheStruct(self.dtype, nb, bs, hkv, rb // elem_bytes(self.dtype),
                            self.k_cache.data_ptr(), self.v_cache.data_ptr(),
@@ -272,7 +345,9 @@ class PagedKVCache:
                            self.v_scale.data_ptr() if self.v_scale is not None else None,
                            self.k_scale_tok.data_ptr() if self.k_scale_tok is not None else None,
                            self.v_scale_tok.data_ptr() if self.v_scale_tok is not None else None,
-                           1 if self.scale_per_layer else 0)
+                           1 if self.scale_per_layer else 0,
+                           self.k_scale_blk.data_ptr() if self.k_scale_blk is not None else None,
+                           self.v_scale_blk.data_ptr() if self.v_scale_blk is not None else None)
 
 
 def kv_write_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
@@ -285,6 +360,28 @@ def kv_write_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
     _check(_lib().pkvq_kv_write_quant(ctypes.byref(cs), _ptr(k), _ptr(v), _ptr(slot_mapping),
                                       int(slot_mapping.shape[0]), _stream(stream)),
            "kv_write_quant")
+
+
+def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
+                         cu_seqlens_new: torch.Tensor, block_table: torch.Tensor,
+                         context_lens: torch.Tensor, max_new_len: int, stream=None) -> None:
+    """Quantizes fp16 K/V [T][Hkv][D], the last cu[b + 1] - cu[b] positions of
+    every sequence b (packed), into a block-scaled cache; context_lens counts
+    them.  A block's scale covers the tokens written to it: it grows when a
+    louder token arrives, and the block's older codes are rounded again."""
+    B = int(context_lens.shape[0])
+    cs = cache.struct()
+    dev = cache.k_cache.get_device()
+    _args(dev, k=(k, torch.float16, (k.shape[0], cache.num_kv_heads, cache.head_dim)),
+          v=(v, torch.float16, tuple(k.shape)),
+          cu_seqlens_new=(cu_seqlens_new, torch.int32, (B + 1,)),
+          block_table=(block_table, torch.int32, (B, block_table.shape[-1])),
+          context_lens=(context_lens, torch.int32, (B,)))
+    with _on(k, stream):
+        _check(_lib().pkvq_kv_write_block_quant(
+            ctypes.byref(cs), _ptr(k), _ptr(v), _ptr(cu_seqlens_new), _ptr(block_table),
+            int(block_table.shape[1]), _ptr(context_lens), B, int(max_new_len),
+            _stream(stream, k.device)), "kv_write_block_quant")
 
 
 def decode_workspace_bytes(cache: PagedKVCache, batch: int, q_len: int, num_q_heads: int,
@@ -313,27 +410,122 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
     _need(block_table, torch.int32, "block_table", 2)
     _need(context_lens, torch.int32, "context_lens", 1)
     B, q_len, Hq, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.float16, "out", 4)
-    if lse is not None:
-        _need(lse, torch.float32, "lse", 3)
     if query_pos is not None:
         _need(query_pos, torch.int32, "query_pos", 2)
         if tuple(query_pos.shape) != (B, q_len):
             raise ValueError("query_pos must be [batch][q_len]")
-    need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len) if B else 0
-    if workspace is None and need:   # contents need not be initialised
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     cs = cache.struct()
-    opts = _opts(sliding_window, query_pos)
-    _check(_lib().pkvq_paged_attn_decode_ex(
-        ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(block_table),
-        int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq, int(max_context_len),
-        float(softmax_scale), None if opts is None else ctypes.byref(opts), _ptr(workspace),
-        wbytes, _stream(stream)), "paged_attn_decode")
+    if D != cs.head_dim:
+        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, torch.float16, "out", 4)
+        if lse is not None:
+            _need(lse, torch.float32, "lse", 3)
+        _batch(B, q, out, lse, block_table, context_lens)
+        if workspace is None and B:   # contents need not be initialised
+            need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        opts = _opts(sliding_window, query_pos)
+        _check(_lib().pkvq_paged_attn_decode_ex(
+            ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(block_table),
+            int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq, int(max_context_len),
+            float(softmax_scale), None if opts is None else ctypes.byref(opts), _ptr(workspace),
+            wbytes, _stream(stream)), "paged_attn_decode")
     return out
+
+
+def decode_weights_workspace_bytes(cache: PagedKVCache, batch: int, q_len: int,
+                                   num_q_heads: int, max_context_len: int) -> int:
+    cs = cache.struct()
+    with _on(cache.k_cache):
+        return int(_lib().pkvq_decode_weights_workspace_bytes(
+            batch, q_len, num_q_heads, max_context_len, ctypes.byref(cs)))
+
+
+def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Tensor,
+                              context_lens: torch.Tensor, max_context_len: int,
+                              softmax_scale: float, weights: torch.Tensor,
+                              out: Optional[torch.Tensor] = None,
+                              lse: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, stream=None,
+                              sliding_window: int = 0) -> torch.Tensor:
+    """paged_attn_decode that also adds every key's softmax weight, summed over
+    the query rows of its KV head, to weights fp32 [B][Hkv][>= max_context_len]
+    (zero the entries of new tokens).  Input of kv_evict."""
+    cs = cache.struct()
+    dev = cache.k_cache.get_device()
+    _need(q, torch.float16, "q", 4)
+    B, q_len, Hq, D = q.shape
+    if D != cs.head_dim:
+        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _args(dev, q=(q, torch.float16, (B, q_len, Hq, D)),
+              out=(out, torch.float16, (B, q_len, Hq, D)), lse=(lse, torch.float32, (B, q_len, Hq)),
+              block_table=(block_table, torch.int32, (B, block_table.shape[-1])),
+              context_lens=(context_lens, torch.int32, (B,)),
+              weights=(weights, torch.float32, (B, cache.num_kv_heads, weights.shape[-1])))
+        if workspace is None and B:   # contents need not be initialised
+            need = decode_weights_workspace_bytes(cache, B, q_len, Hq, max_context_len)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        wbytes = 0
+        if workspace is not None:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+            wbytes = workspace.numel() * workspace.element_size()
+        opts = _opts(sliding_window, None)
+        _check(_lib().pkvq_paged_attn_decode_weights(
+            ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(block_table),
+            int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq, int(max_context_len),
+            float(softmax_scale), None if opts is None else ctypes.byref(opts), _ptr(weights),
+            int(weights.shape[2]), _ptr(workspace), wbytes, _stream(stream, q.device)),
+            "paged_attn_decode_weights")
+    return out
+
+
+def kv_evict(cache: PagedKVCache, weights: torch.Tensor, block_table: torch.Tensor,
+             context_lens: torch.Tensor, dst_block_table: torch.Tensor, budget: int,
+             num_sink: int = 0, num_recent: int = 0,
+             weights_out: Optional[torch.Tensor] = None, keep: Optional[torch.Tensor] = None,
+             new_context_lens: Optional[torch.Tensor] = None, stream=None):
+    """Keeps at most `budget` tokens of every (sequence, KV head) -- the first
+    num_sink, the last num_recent and the heaviest others by weights fp32
+    [B][Hkv][W] -- and moves them, in order, to the blocks of dst_block_table
+    (distinct blocks that hold no token of these sequences).
+    Returns (new_context_lens int32 [B], weights_out fp32 [B][Hkv][W'], keep
+    int32 [B][Hkv][budget]: the kept positions, -1 behind the last)."""
+    cs = cache.struct()
+    dev = cache.k_cache.get_device()
+    B, H = int(context_lens.shape[0]), cache.num_kv_heads
+    budget = int(budget)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    with _on(weights, stream):
+        if weights_out is None:
+            weights_out = torch.empty((B, H, max(weights.shape[-1], budget)), dtype=torch.float32,
+                                      device=weights.device)
+        if keep is None:
+            keep = torch.empty((B, H, budget), dtype=torch.int32, device=weights.device)
+        if new_context_lens is None:
+            new_context_lens = torch.empty_like(context_lens)
+        _args(dev, weights=(weights, torch.float32, (B, H, weights.shape[-1])),
+              block_table=(block_table, torch.int32, (B, block_table.shape[-1])),
+              context_lens=(context_lens, torch.int32, (B,)),
+              dst_block_table=(dst_block_table, torch.int32, (B, dst_block_table.shape[-1])),
+              weights_out=(weights_out, torch.float32, (B, H, weights_out.shape[-1])),
+              keep=(keep, torch.int32, (B, H, budget)),
+              new_context_lens=(new_context_lens, torch.int32, (B,)))
+        _check(_lib().pkvq_kv_evict(
+            ctypes.byref(cs), _ptr(weights), int(weights.shape[2]), _ptr(block_table),
+            int(block_table.shape[1]), _ptr(context_lens), B, budget, int(num_sink),
+            int(num_recent), _ptr(dst_block_table), int(dst_block_table.shape[1]), _ptr(keep),
+            _ptr(new_context_lens), _ptr(weights_out), int(weights_out.shape[2]),
+            _stream(stream, weights.device)), "kv_evict")
+    return new_context_lens, weights_out, keep
 
 
 def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -355,22 +547,27 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
     B, q_len, Hq, D = q.shape
     if tuple(k_new.shape) != (B, q_len, cache.num_kv_heads, D) or k_new.shape != v_new.shape:
         raise ValueError("k_new / v_new must be [batch][q_len][num_kv_heads][head_dim]")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.float16, "out", 4)
-    if lse is not None:
-        _need(lse, torch.float32, "lse", 3)
-    need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len) if B else 0
-    if workspace is None and need:   # contents need not be initialised
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     cs = cache.struct()
-    opts = _opts(sliding_window, None)
-    _check(_lib().pkvq_paged_attn_decode_append(
-        ctypes.byref(cs), _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(out), _ptr(lse),
-        _ptr(block_table), int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq,
-        int(max_context_len), float(softmax_scale), None if opts is None else ctypes.byref(opts),
-        _ptr(workspace), wbytes, _stream(stream)), "paged_attn_decode_append")
+    if D != cs.head_dim:
+        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, torch.float16, "out", 4)
+        if lse is not None:
+            _need(lse, torch.float32, "lse", 3)
+        _batch(B, q, out, lse, block_table, context_lens)
+        if workspace is None and B:   # contents need not be initialised
+            need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        opts = _opts(sliding_window, None)
+        _check(_lib().pkvq_paged_attn_decode_append(
+            ctypes.byref(cs), _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(out), _ptr(lse),
+            _ptr(block_table), int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq,
+            int(max_context_len), float(softmax_scale),
+            None if opts is None else ctypes.byref(opts), _ptr(workspace), wbytes,
+            _stream(stream)), "paged_attn_decode_append")
     return out
 
 
@@ -385,19 +582,25 @@ def paged_attn_prefill(cache: PagedKVCache, q: torch.Tensor, cu_seqlens_q: torch
     _need(block_table, torch.int32, "block_table", 2)
     _need(context_lens, torch.int32, "context_lens", 1)
     total_q, Hq, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.float16, "out", 3)
-    if lse is not None:
-        _need(lse, torch.float32, "lse", 2)
     B = int(context_lens.shape[0])
+    if cu_seqlens_q.shape[0] != B + 1:
+        raise ValueError("cu_seqlens_q must have one entry more than context_lens")
     cs = cache.struct()
-    opts = _opts(sliding_window, None)
-    _check(_lib().pkvq_paged_attn_prefill_ex(
-        ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(block_table),
-        int(block_table.shape[1]), _ptr(context_lens), B, int(max_q_len), Hq,
-        float(softmax_scale), None if opts is None else ctypes.byref(opts), None, 0,
-        _stream(stream)), "paged_attn_prefill")
+    if D != cs.head_dim:
+        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, torch.float16, "out", 3)
+        if lse is not None:
+            _need(lse, torch.float32, "lse", 2)
+        _batch(B, q, out, lse, block_table, context_lens)
+        opts = _opts(sliding_window, None)
+        _check(_lib().pkvq_paged_attn_prefill_ex(
+            ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
+            _ptr(block_table), int(block_table.shape[1]), _ptr(context_lens), B, int(max_q_len),
+            Hq, float(softmax_scale), None if opts is None else ctypes.byref(opts), None, 0,
+            _stream(stream)), "paged_attn_prefill")
     return out
 
 

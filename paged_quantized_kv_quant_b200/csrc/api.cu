@@ -19,6 +19,7 @@ __device__ uint32_t g_status_word;
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxGridYZ = 65535;   // CUDA's limit of a grid's y and z
 
 uint32_t *status_ptr()
 {
@@ -62,7 +63,8 @@ pkvq_status check_cache(const pkvq_cache *c)
     if (!c || !c->k_cache || !c->v_cache)
         return PKVQ_ERR_INVALID_ARG;
     if (c->dtype != PKVQ_KV_FP8_E4M3 && c->dtype != PKVQ_KV_INT8 &&
-        c->dtype != PKVQ_KV_FP8_E5M2 && c->dtype != PKVQ_KV_FP16)
+        c->dtype != PKVQ_KV_FP8_E5M2 && c->dtype != PKVQ_KV_FP16 &&
+        c->dtype != PKVQ_KV_INT8_BLOCK && c->dtype != PKVQ_KV_E4M3_BLOCK)
         return PKVQ_ERR_UNSUPPORTED;
     if (c->head_dim != kHeadDim)
         return PKVQ_ERR_UNSUPPORTED;
@@ -80,6 +82,11 @@ pkvq_status check_cache(const pkvq_cache *c)
         if (!c->k_scale_tok || !c->v_scale_tok)
             return PKVQ_ERR_INVALID_ARG;
         if (!aligned16(c->k_scale_tok) || !aligned16(c->v_scale_tok))
+            return PKVQ_ERR_MISALIGNED;
+    } else if (kv_has_block_scale(c->dtype)) {
+        if (!c->k_scale_blk || !c->v_scale_blk)
+            return PKVQ_ERR_INVALID_ARG;
+        if (!aligned16(c->k_scale_blk) || !aligned16(c->v_scale_blk))
             return PKVQ_ERR_MISALIGNED;
     }
     if (!aligned16(c->k_cache) || !aligned16(c->v_cache))
@@ -198,6 +205,8 @@ pkvq_status pkvq_kv_write_quant(const pkvq_cache *cache, const void *k, const vo
     pkvq_status st = check_cache(cache);
     if (st != PKVQ_OK)
         return st;
+    if (kv_has_block_scale(cache->dtype))
+        return PKVQ_ERR_UNSUPPORTED;   // pkvq_kv_write_block_quant
     if (num_tokens < 0)
         return PKVQ_ERR_INVALID_ARG;
     if (num_tokens == 0)
@@ -227,6 +236,65 @@ pkvq_status pkvq_kv_write_quant(const pkvq_cache *cache, const void *k, const vo
     return from_cuda(launch_kv_write_quant(p, cache->dtype, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+KvWriteBlockParams block_write_params(const pkvq_cache *cache, const void *k, const void *v,
+                                      const int32_t *cu_seqlens_new, const int32_t *block_table,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                      int32_t batch, int32_t max_new_len, uint32_t *status)
+{
+    KvWriteBlockParams p{};
+    p.k_cache = static_cast<uint8_t *>(cache->k_cache);
+    p.v_cache = static_cast<uint8_t *>(cache->v_cache);
+    p.k_scale_blk = cache->k_scale_blk;
+    p.v_scale_blk = cache->v_scale_blk;
+    p.k = static_cast<const __half *>(k);
+    p.v = static_cast<const __half *>(v);
+    p.cu_seqlens_new = cu_seqlens_new;
+    p.block_table = block_table;
+    p.context_lens = context_lens;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.batch = batch;
+    p.max_new_len = p.q_len = max_new_len;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.num_blocks = cache->num_blocks;
+    p.block_size = cache->block_size;
+    p.status = status;
+    return p;
+}
+
+}  // namespace
+
+pkvq_status pkvq_kv_write_block_quant(const pkvq_cache *cache, const void *k, const void *v,
+                                      const int32_t *cu_seqlens_new, const int32_t *block_table,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                      int32_t batch, int32_t max_new_len, void *stream)
+{
+    pkvq_status st = check_cache(cache);
+    if (st != PKVQ_OK)
+        return st;
+    if (!kv_has_block_scale(cache->dtype))
+        return PKVQ_ERR_UNSUPPORTED;   // pkvq_kv_write_quant
+    if (batch < 0 || max_new_len < 0 || max_blocks_per_seq < 0)
+        return PKVQ_ERR_INVALID_ARG;
+    if (batch == 0 || max_new_len == 0)
+        return PKVQ_OK;
+    if (!k || !v || !cu_seqlens_new || !block_table || !context_lens)
+        return PKVQ_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v))
+        return PKVQ_ERR_MISALIGNED;
+    if ((((long long)max_new_len + cache->block_size - 2) / cache->block_size + 1) * batch >=
+            (1LL << 31) || cache->num_kv_heads > kMaxGridYZ)
+        return PKVQ_ERR_UNSUPPORTED;   // the launch grid
+    uint32_t *status = status_ptr();
+    if (!status)
+        return PKVQ_ERR_CUDA;
+    return from_cuda(launch_kv_write_block(
+        block_write_params(cache, k, v, cu_seqlens_new, block_table, max_blocks_per_seq,
+                           context_lens, batch, max_new_len, status),
+        cache->dtype, static_cast<cudaStream_t>(stream)));
+}
+
 size_t pkvq_decode_workspace_bytes(int32_t batch, int32_t q_len, int32_t num_q_heads,
                                    int32_t max_context_len, const pkvq_cache *cache)
 {
@@ -235,7 +303,21 @@ size_t pkvq_decode_workspace_bytes(int32_t batch, int32_t q_len, int32_t num_q_h
         return 0;
     DecodePlan plan;
     if (!decode_plan(cache->dtype, batch, q_len, num_q_heads, cache->num_kv_heads, cache->block_size,
-                     max_context_len, &plan))
+                     max_context_len, false, &plan))
+        return 0;
+    return plan.workspace_bytes;
+}
+
+size_t pkvq_decode_weights_workspace_bytes(int32_t batch, int32_t q_len, int32_t num_q_heads,
+                                           int32_t max_context_len, const pkvq_cache *cache)
+{
+    if (check_cache(cache) != PKVQ_OK || batch <= 0 || q_len <= 0 || q_len > 16 ||
+        max_context_len < 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads ||
+        num_q_heads / cache->num_kv_heads > 16)
+        return 0;
+    DecodePlan plan;
+    if (!decode_plan(cache->dtype, batch, q_len, num_q_heads, cache->num_kv_heads, cache->block_size,
+                     max_context_len, true, &plan))
         return 0;
     return plan.workspace_bytes;
 }
@@ -261,7 +343,8 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
                         int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
                         int32_t q_len, int32_t num_q_heads, int32_t max_context_len,
                         float softmax_scale, const pkvq_attn_opts *opts, void *workspace,
-                        size_t workspace_bytes, void *stream)
+                        size_t workspace_bytes, void *stream, float *weights = nullptr,
+                        int64_t weight_stride = 0)
 {
     if (opts && opts->sliding_window < 0)
         return PKVQ_ERR_INVALID_ARG;
@@ -288,7 +371,7 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
         return PKVQ_ERR_INVALID_ARG;
     DecodePlan plan;
     if (!decode_plan(cache->dtype, batch, q_len, num_q_heads, cache->num_kv_heads, cache->block_size,
-                     max_context_len, &plan))
+                     max_context_len, weights != nullptr, &plan))
         return PKVQ_ERR_INVALID_ARG;
     if (plan.workspace_bytes > 0) {
         if (!workspace || workspace_bytes < plan.workspace_bytes)
@@ -309,6 +392,8 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
     p.scale_stride = scale_stride(cache);
     p.k_scale_tok = static_cast<const uint16_t *>(cache->k_scale_tok);
     p.v_scale_tok = static_cast<const uint16_t *>(cache->v_scale_tok);
+    p.k_scale_blk = cache->k_scale_blk;
+    p.v_scale_blk = cache->v_scale_blk;
     p.window = opts ? opts->sliding_window : 0;
     p.query_pos = opts ? opts->query_pos : nullptr;
     p.q = static_cast<const __half *>(q);
@@ -343,8 +428,27 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
     if (!p.status)
         return PKVQ_ERR_CUDA;
     cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+    if (weights) {
+        p.scores = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + plan.state_bytes);
+        p.weights = weights;
+        p.weight_stride = weight_stride;
+        p.score_keys = plan.score_keys;
+        p.score_rows = plan.score_rows;
+        return from_cuda(launch_decode_weights(p, plan, cache->dtype, km, vm, st_));
+    }
     if (k_new) {
-        if (plan.tc) {
+        if (kv_has_block_scale(cache->dtype)) {
+            // a block's scale follows from all its new tokens: the block
+            // write kernel runs just before
+            if (cache->num_kv_heads > kMaxGridYZ || (2LL + q_len / 16) * batch >= (1LL << 31))
+                return PKVQ_ERR_UNSUPPORTED;
+            const cudaError_t e = launch_kv_write_block(
+                block_write_params(cache, k_new, v_new, nullptr, block_table, max_blocks_per_seq,
+                                   context_lens, batch, q_len, p.status),
+                cache->dtype, st_);
+            if (e != cudaSuccess)
+                return from_cuda(e);
+        } else if (plan.tc) {
             // the tensor-core kernel reads whole tiles through one copy ring:
             // the new tokens are written by the KV write kernel just before
             KvWriteParams w{};
@@ -417,6 +521,79 @@ pkvq_status pkvq_paged_attn_decode_append(const pkvq_cache *cache, const void *k
                        opts, workspace, workspace_bytes, stream);
 }
 
+pkvq_status pkvq_paged_attn_decode_weights(const pkvq_cache *cache, const void *q, void *out,
+                                           float *lse_out, const int32_t *block_table,
+                                           int32_t max_blocks_per_seq,
+                                           const int32_t *context_lens, int32_t batch,
+                                           int32_t q_len, int32_t num_q_heads,
+                                           int32_t max_context_len, float softmax_scale,
+                                           const pkvq_attn_opts *opts, float *weights,
+                                           int64_t weight_stride, void *workspace,
+                                           size_t workspace_bytes, void *stream)
+{
+    if (batch > 0 && (!weights || weight_stride < max_context_len))
+        return PKVQ_ERR_INVALID_ARG;
+    if (cache && (batch > kMaxGridYZ || cache->num_kv_heads > kMaxGridYZ))
+        return PKVQ_ERR_UNSUPPORTED;   // the weights kernel's grid
+    return decode_impl(cache, nullptr, nullptr, q, out, lse_out, block_table, max_blocks_per_seq,
+                       context_lens, batch, q_len, num_q_heads, max_context_len, softmax_scale,
+                       opts, workspace, workspace_bytes, stream, weights, weight_stride);
+}
+
+pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights, int64_t weight_stride,
+                          const int32_t *block_table, int32_t max_blocks_per_seq,
+                          const int32_t *context_lens, int32_t batch, int32_t budget,
+                          int32_t num_sink, int32_t num_recent, const int32_t *dst_block_table,
+                          int32_t dst_max_blocks, int32_t *keep_out, int32_t *new_context_lens,
+                          float *weights_out, int64_t weight_out_stride, void *stream)
+{
+    pkvq_status st = check_cache(cache);
+    if (st != PKVQ_OK)
+        return st;
+    if (batch < 0 || budget < 1 || num_sink < 0 || num_recent < 0 ||
+        (long long)num_sink + num_recent > budget || max_blocks_per_seq < 0 ||
+        dst_max_blocks < 0 || (long long)dst_max_blocks * cache->block_size < budget ||
+        weight_stride < 0 || (weights_out && weight_out_stride < budget))
+        return PKVQ_ERR_INVALID_ARG;
+    if (batch > kMaxGridYZ || cache->num_kv_heads > kMaxGridYZ)
+        return PKVQ_ERR_UNSUPPORTED;   // the launch grid
+    if (batch == 0)
+        return PKVQ_OK;
+    if (!weights || !block_table || !context_lens || !dst_block_table || !keep_out ||
+        !new_context_lens || weights_out == weights || new_context_lens == context_lens)
+        return PKVQ_ERR_INVALID_ARG;
+    EvictParams p{};
+    p.k_cache = static_cast<uint8_t *>(cache->k_cache);
+    p.v_cache = static_cast<uint8_t *>(cache->v_cache);
+    p.k_scale_tok = static_cast<uint16_t *>(cache->k_scale_tok);
+    p.v_scale_tok = static_cast<uint16_t *>(cache->v_scale_tok);
+    p.k_scale_blk = cache->k_scale_blk;
+    p.v_scale_blk = cache->v_scale_blk;
+    p.weights = weights;
+    p.weight_stride = weight_stride;
+    p.weights_out = weights_out;
+    p.weight_out_stride = weight_out_stride;
+    p.block_table = block_table;
+    p.context_lens = context_lens;
+    p.dst_block_table = dst_block_table;
+    p.keep = keep_out;
+    p.new_context_lens = new_context_lens;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.dst_max_blocks = dst_max_blocks;
+    p.block_size = cache->block_size;
+    p.batch = batch;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.num_blocks = cache->num_blocks;
+    p.budget = budget;
+    p.sink = num_sink;
+    p.recent = num_recent;
+    p.status = status_ptr();
+    if (!p.status)
+        return PKVQ_ERR_CUDA;
+    return from_cuda(launch_evict(p, cache->dtype, cache->block_size,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
 pkvq_status pkvq_paged_attn_prefill(const pkvq_cache *cache, const void *q, void *out,
                                     float *lse_out, const int32_t *cu_seqlens_q,
                                     const int32_t *block_table, int32_t max_blocks_per_seq,
@@ -474,6 +651,8 @@ pkvq_status pkvq_paged_attn_prefill_ex(const pkvq_cache *cache, const void *q, v
     p.k_scale = head_scale ? cache->k_scale : nullptr;
     p.v_scale = head_scale ? cache->v_scale : nullptr;
     p.scale_stride = scale_stride(cache);
+    p.k_scale_blk = cache->k_scale_blk;
+    p.v_scale_blk = cache->v_scale_blk;
     p.window = opts ? opts->sliding_window : 0;
     p.k_scale_tok = static_cast<const uint16_t *>(cache->k_scale_tok);
     p.v_scale_tok = static_cast<const uint16_t *>(cache->v_scale_tok);
@@ -552,6 +731,12 @@ pkvq_status pkvq_kv_copy_blocks(const pkvq_cache *dst, const pkvq_cache *src,
     p.src_vs = int8 ? static_cast<const uint16_t *>(src->v_scale_tok) : nullptr;
     p.dst_ks = int8 ? static_cast<uint16_t *>(dst->k_scale_tok) : nullptr;
     p.dst_vs = int8 ? static_cast<uint16_t *>(dst->v_scale_tok) : nullptr;
+    const bool blk = kv_has_block_scale(src->dtype);
+    p.src_kb = blk ? src->k_scale_blk : nullptr;
+    p.src_vb = blk ? src->v_scale_blk : nullptr;
+    p.dst_kb = blk ? dst->k_scale_blk : nullptr;
+    p.dst_vb = blk ? dst->v_scale_blk : nullptr;
+    p.num_kv_heads = src->num_kv_heads;
     p.pairs = pairs;
     p.n = n;
     p.block_bytes = (long long)src->num_kv_heads * src->block_size * kHeadDim *

@@ -47,6 +47,11 @@
 // an FP32 partial (unnormalised O, max in log2 units, sum) in the decode
 // workspace, which the decode merge kernel combines.
 //
+// Block-scaled formats (a K and a V scale per block and KV head): the K warps
+// hand the softmax each key's score factor, the V warps log2 of its V scale;
+// the softmax takes p' = 2^(s + log2 vs - M), l += p' / vs, and the codes enter
+// the tensor core exactly.
+//
 // FP16 caches need no conversion: warp 9 copies each key's two 128-byte row
 // halves straight into a K/V buffer (the same swizzled layout) with cp.async,
 // and the dequant warps only clear the rows past the context or the split
@@ -101,7 +106,10 @@ constexpr int kOffCodes = kOffKV + kKVBufs * kKVBuf;
 constexpr int kCodeStage = 16384;
 constexpr int kOffScl = kOffCodes + kCodeStages * kCodeStage;   // stages x 8 warps x 32 halves (16 used)
 constexpr int kOffKsf = kOffScl + kCodeStages * kDequantWarps * 64;   // bufs x 64 fp32 K factors
-constexpr int kOffBars = kOffKsf + kKVBufs * 64 * 4;
+// block-scaled formats: bufs x 64 fp32 log2 V scales, bufs x 4 fp32 1 / V scale (16 keys each)
+constexpr int kOffLvf = kOffKsf + kKVBufs * 64 * 4;
+constexpr int kOffIvf = kOffLvf + kKVBufs * 64 * 4;
+constexpr int kOffBars = kOffIvf + kKVBufs * 4 * 4;
 constexpr int kNumBars = 1 + 3 * kKVBufs + 3 * kSBufs + 2;
 constexpr int kOffTaddr = kOffBars + kNumBars * 8;
 constexpr int kOffProgress = kOffTaddr + 8;   // tiles dequantised so far (prefetch pacing)
@@ -151,7 +159,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32
 template <int KVT>
 __device__ __forceinline__ void cvt4(uint32_t x, uint32_t &lo, uint32_t &hi)
 {
-    if constexpr (KVT == kKvFp8)
+    if constexpr (KVT == kKvFp8 || KVT == kKvE4m3Blk)
         e4m3x4_to_half2x2(x, lo, hi);
     else if constexpr (KVT == kKvE5m2)
         e5m2x4_to_half2x2(x, lo, hi);
@@ -225,7 +233,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     if (warp == kWarpPf) {
         // -------------------------------------------- L2 prefetch / copies --
         const CacheView cv{p.k_cache, p.v_cache, p.k_scale_tok, p.v_scale_tok, p.num_kv_heads,
-                           p.num_blocks, p.status};
+                           p.num_blocks, p.status, p.k_scale_blk, p.v_scale_blk};
         BlockWindow w;
         // every index stays inside the table row, even for a context longer
         // than the row can address (a caller error: those keys read block 0)
@@ -414,6 +422,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     if (KVT == kKvInt8 && lane < 2)   // 8 rows' scales per lane
                         cp_async_16(sbase + kOffScl + (st * kDequantWarps + warp) * 64 + 16 * lane,
                                     scl + y0 + 8 * lane);
+                    if (kv_has_block_scale(KVT) && lane == 0)   // the scale of the rows' block
+                        cp_async_4(sbase + kOffScl + (st * kDequantWarps + warp) * 64,
+                                   (isv ? p.v_scale_blk : p.k_scale_blk) +
+                                       (size_t)phys * p.num_kv_heads + h);
                 }
                 cp_async_commit();
             };
@@ -476,6 +488,21 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         float *ksf = reinterpret_cast<float *>(smem + kOffKsf) + bj * 64;
                         ksf[row] =
                             live ? kfac * __half2float(__ushort_as_half((uint16_t)sc)) : 0.0f;
+                    }
+                }
+                if constexpr (kv_has_block_scale(KVT)) {
+                    const float sb = *reinterpret_cast<const float *>(
+                        smem + kOffScl + (st * kDequantWarps + warp) * 64);
+                    if (!isv && dh == 0)
+                        reinterpret_cast<float *>(smem + kOffKsf)[bj * 64 + row] =
+                            live ? kfac * sb : 0.0f;
+                    if (isv && dh == 0) {
+                        // scale 0: every code of the block is 0, any factor serves
+                        const float vs = live && sb > 0.0f ? sb : 1.0f;
+                        reinterpret_cast<float *>(smem + kOffLvf)[bj * 64 + row] = log2f(vs);
+                        if (lane == 0)
+                            reinterpret_cast<float *>(smem + kOffIvf)[bj * 4 + (warp & 3)] =
+                                __frcp_rn(vs);
                     }
                 }
                 fence_async_smem();
@@ -550,7 +577,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 ok = false;
                 break;
             }
-            if constexpr (KVT == kKvInt8) {
+            if constexpr (KVT == kKvInt8 || kv_has_block_scale(KVT)) {
                 // the per-key factors below were written by the dequant warps
                 if (!warp_wait(&bars.kv_full[j % kKVBufs], (j / kKVBufs) & 1, p.status)) {
                     ok = false;
@@ -576,7 +603,19 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             }
             const int tile0 = key_begin + j * kKT;   // first key of the tile
             const int key0 = tile0 + kh * kCols;     // first key of this thread's scores
-            if constexpr (KVT != kKvInt8) {
+            if constexpr (kv_has_block_scale(KVT)) {
+                const float *ksf =
+                    reinterpret_cast<const float *>(smem + kOffKsf) + (j % kKVBufs) * 64 + kh * kCols;
+                const float *lvf =
+                    reinterpret_cast<const float *>(smem + kOffLvf) + (j % kKVBufs) * 64 + kh * kCols;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2) {
+                    const float2 r2 = __ffma2_rn(make_float2(v[c], v[c + 1]),
+                                                 make_float2(ksf[c], ksf[c + 1]),
+                                                 make_float2(lvf[c], lvf[c + 1]));
+                    v[c] = r2.x, v[c + 1] = r2.y;
+                }
+            } else if constexpr (KVT != kKvInt8) {
                 const float2 f2 = make_float2(kfac, kfac);
 #pragma unroll
                 for (int c = 0; c < kCols; c += 2) {
@@ -655,7 +694,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const int cc = 32 * g + c;
                     const float2 d = __fadd2_rn(make_float2(v[cc], v[cc + 1]), nmu);
                     const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-                    acc[(c >> 1) & 3] = __fadd2_rn(acc[(c >> 1) & 3], e);
+                    // (block-scaled: one sum for each 16 keys, which share a V scale)
+                    const int ai = kv_has_block_scale(KVT) ? cc >> 4 : (c >> 1) & 3;
+                    acc[ai] = __fadd2_rn(acc[ai], e);
                     pk[c / 2] = pack_half2(e.x, e.y);
                 }
                 if constexpr (kHalf)
@@ -663,9 +704,17 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 else
                     tmem_st16(tl + kTmS + sbuf(j) * kKT + 16 * g, pk);
             }
-            const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-            const float2 a = __fadd2_rn(a01, a23);
-            l += a.x + a.y;
+            if constexpr (kv_has_block_scale(KVT)) {
+                const float *ivf = reinterpret_cast<const float *>(smem + kOffIvf) +
+                                   (j % kKVBufs) * 4 + kh * (kCols / 16);
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i)
+                    l = fmaf(acc[i].x + acc[i].y, ivf[i], l);
+            } else {
+                const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+                const float2 a = __fadd2_rn(a01, a23);
+                l += a.x + a.y;
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -776,6 +825,8 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int kv_dtype, const CUtensor
         PKVQ_TC_CASE(kKvInt8, 16) PKVQ_TC_CASE(kKvInt8, 32) PKVQ_TC_CASE(kKvInt8, 64)
         PKVQ_TC_CASE(kKvE5m2, 16) PKVQ_TC_CASE(kKvE5m2, 32) PKVQ_TC_CASE(kKvE5m2, 64)
         PKVQ_TC_CASE(kKvFp16, 16) PKVQ_TC_CASE(kKvFp16, 32) PKVQ_TC_CASE(kKvFp16, 64)
+        PKVQ_TC_CASE(kKvInt8Blk, 16) PKVQ_TC_CASE(kKvInt8Blk, 32) PKVQ_TC_CASE(kKvInt8Blk, 64)
+        PKVQ_TC_CASE(kKvE4m3Blk, 16) PKVQ_TC_CASE(kKvE4m3Blk, 32) PKVQ_TC_CASE(kKvE4m3Blk, 64)
 #undef PKVQ_TC_CASE
     default: return cudaErrorInvalidValue;
     }

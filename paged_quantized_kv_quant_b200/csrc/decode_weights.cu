@@ -1,0 +1,188 @@
+// Decode attention that also accumulates every key's softmax weight, for
+// eviction by accumulated attention weight.
+//
+// Mathematics.  With s_rj the scaled score of query row r and key j and
+// lse_r = ln sum_j e^s_rj, the weight of key j in KV head h is
+//   W[j] += sum over the KV head's rows r = (query token, query head) of
+//           e^(s_rj - lse_r).
+// The normaliser is known only after the last split, so the split kernel
+// stores the scores it has in registers (fp32, log2 units) and a second kernel
+// turns them into weights: 4 bytes written and read per (row, key), which with
+// 8 rows is a quarter of the 256 bytes of K and V, and mostly stays in the
+// 126 MB L2; reading K again for a second Q K^T would cost 128 bytes per key
+// from DRAM.  No atomics: every W element has one writer, so results do not
+// depend on the order of CTAs.
+#include "decode_split.cuh"
+
+namespace pkvq {
+namespace {
+
+constexpr int kWThreads = 256;
+constexpr int kKeysPerThread = 2;
+constexpr int kChunk = kWThreads * kKeysPerThread;
+constexpr int kMaxRows = 256;   // 16 query tokens x 16 heads per KV head
+
+// Grid: x < chunks: keys [x * kChunk, ...) of (KV head y, sequence z); the
+// remaining CTAs merge the partial states of 8 output rows each.
+// RR: score rows per key (1, 2, 4, 8), or 0 for any multiple of 4.
+template <int BS, int RR>
+__global__ void __launch_bounds__(kWThreads)
+decode_weights_kernel(const DecodeParams p, const int chunks)
+{
+    __shared__ float lse2[kMaxRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, b = blockIdx.z;
+    // The next call's kernels wait for this grid's completion themselves.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const SplitInfo si = find_split<BS>(p, -1, b);
+    // the split kernel's partial states and scores
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if ((int)blockIdx.x >= chunks) {
+        const int rr = ((int)blockIdx.x - chunks) * (kWThreads / 32) + warp;
+        if (rr < p.rows && si.nsplit > 1) {   // (a single split wrote the final row itself)
+            MergeRow mr;
+            mr.row0 = (size_t)((rr / p.rows_per_cta) * p.num_kv_heads + h) * p.num_splits *
+                          p.rows_per_cta + rr % p.rows_per_cta;
+            mr.stride = p.rows_per_cta;
+            mr.load(p, si.first, si.nsplit, 0, lane);
+            mr.finish(p, si.first, si.nsplit, b, h, rr, lane);
+        }
+        return;
+    }
+
+    const int R = RR ? RR : p.score_rows;
+    const int lo = si.blk0 * BS;   // scores exist for keys lo .. ctx - 1
+    const int hi = min(si.ctx, min(p.score_keys, (int)min(p.weight_stride, (long long)INT_MAX)));
+    const int c0 = blockIdx.x * kChunk;
+    if (c0 >= hi || c0 + kChunk <= lo)
+        return;   // (a CTA-wide decision)
+    const float *sc = p.scores + ((size_t)b * p.num_kv_heads + h) * p.score_keys * R;
+    float *W = p.weights + ((size_t)b * p.num_kv_heads + h) * p.weight_stride;
+
+    // this thread's scores and weights are on their way while the row
+    // normalisers are combined
+    float v[kKeysPerThread][RR ? RR : 1], w[kKeysPerThread];
+#pragma unroll
+    for (int k = 0; k < kKeysPerThread; ++k) {
+        const int key = c0 + k * kWThreads + threadIdx.x;
+        w[k] = 0.0f;
+        if (key >= lo && key < hi) {
+            w[k] = W[key];
+            if constexpr (RR != 0) {
+                const float *src = sc + (size_t)key * RR;
+                if constexpr (RR >= 4) {
+#pragma unroll
+                    for (int i = 0; i < RR; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(src + i);
+                        v[k][i] = x.x, v[k][i + 1] = x.y, v[k][i + 2] = x.z, v[k][i + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RR; ++i)
+                        v[k][i] = src[i];
+                }
+            }
+        }
+    }
+    // log2-sum-exp2 of every row from its splits' (max, sum) states; rows
+    // that see no key (and padding rows) get +inf: weight 0
+    for (int r = warp; r < R; r += kWThreads / 32) {
+        float M = -INFINITY, L = 0.0f;
+        if (r < p.rows) {
+            const size_t row0 = (size_t)((r / p.rows_per_cta) * p.num_kv_heads + h) *
+                                    p.num_splits * p.rows_per_cta + r % p.rows_per_cta;
+            for (int s = lane; s < si.nsplit; s += 32) {
+                const float2 ml = *reinterpret_cast<const float2 *>(
+                    p.ws_ml + (row0 + (size_t)(si.first + s) * p.rows_per_cta) * 2);
+                const float m = fmaxf(M, ml.x), mu = m == -INFINITY ? 0.0f : m;
+                L = L * fast_exp2(M - mu) + ml.y * fast_exp2(ml.x - mu);
+                M = m;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, M, o);
+            const float l2 = __shfl_xor_sync(0xffffffffu, L, o);
+            const float m = fmaxf(M, m2), mu = m == -INFINITY ? 0.0f : m;
+            L = L * fast_exp2(M - mu) + l2 * fast_exp2(m2 - mu);
+            M = m;
+        }
+        if (lane == 0)
+            lse2[r] = L > 0.0f ? M + log2f(L) : INFINITY;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kKeysPerThread; ++k) {
+        const int key = c0 + k * kWThreads + threadIdx.x;
+        if (key < lo || key >= hi)
+            continue;
+        float a = 0.0f;
+        if constexpr (RR != 0) {
+#pragma unroll
+            for (int i = 0; i < RR; ++i)
+                a += fast_exp2(v[k][i] - lse2[i]);
+        } else {
+            const float4 *src = reinterpret_cast<const float4 *>(sc + (size_t)key * R);
+            for (int i = 0; i < R; i += 4) {
+                const float4 x = src[i / 4];
+                a += (fast_exp2(x.x - lse2[i]) + fast_exp2(x.y - lse2[i + 1])) +
+                     (fast_exp2(x.z - lse2[i + 2]) + fast_exp2(x.w - lse2[i + 3]));
+            }
+        }
+        W[key] = w[k] + a;
+    }
+}
+
+template <int BS, int RR>
+cudaError_t launch_w(const DecodeParams &p, cudaStream_t stream)
+{
+    const int chunks = (p.score_keys + kChunk - 1) / kChunk;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(chunks + (p.rows + kWThreads / 32 - 1) / (kWThreads / 32)),
+                       (unsigned)p.num_kv_heads, (unsigned)p.batch);
+    cfg.blockDim = dim3(kWThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_weights_kernel<BS, RR>, p, chunks);
+}
+
+template <int BS>
+cudaError_t launch_rr(const DecodeParams &p, cudaStream_t stream)
+{
+    switch (p.score_rows) {
+    case 1: return launch_w<BS, 1>(p, stream);
+    case 2: return launch_w<BS, 2>(p, stream);
+    case 4: return launch_w<BS, 4>(p, stream);
+    case 8: return launch_w<BS, 8>(p, stream);
+    default: return launch_w<BS, 0>(p, stream);
+    }
+}
+
+}  // namespace
+
+int weights_split_occupancy(int kv_dtype, int nt, int block_size)
+{
+    return split_occupancy_any<true>(kv_dtype, nt, block_size);
+}
+
+cudaError_t launch_decode_weights(const DecodeParams &p, const DecodePlan &plan, int kv_dtype,
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                  cudaStream_t stream)
+{
+    cudaError_t e = launch_split_any<true>(kv_dtype, plan.nt, p, kmap, vmap, stream);
+    if (e != cudaSuccess)
+        return e;
+    switch (p.block_size) {
+    case 16: return launch_rr<16>(p, stream);
+    case 32: return launch_rr<32>(p, stream);
+    case 64: return launch_rr<64>(p, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pkvq

@@ -14,6 +14,9 @@ constexpr int kKvFp8 = 0;     // E4M3
 constexpr int kKvInt8 = 1;
 constexpr int kKvE5m2 = 2;
 constexpr int kKvFp16 = 3;
+constexpr int kKvInt8Blk = 4;  // INT8 codes, fp32 scale per (block, KV head)
+constexpr int kKvE4m3Blk = 5;  // E4M3 codes, fp32 scale per (block, KV head)
+constexpr int kNumKvTypes = 6;
 constexpr int kHeadDim = 128;
 
 // Bytes per stored cache element of a format.
@@ -22,6 +25,12 @@ __host__ __device__ constexpr int kv_elem_bytes(int kvt) { return kvt == kKvFp16
 __host__ __device__ constexpr bool kv_has_head_scale(int kvt)
 {
     return kvt == kKvFp8 || kvt == kKvE5m2;
+}
+
+// Formats with an fp32 scale per (block, KV head), written with the tokens.
+__host__ __device__ constexpr bool kv_has_block_scale(int kvt)
+{
+    return kvt == kKvInt8Blk || kvt == kKvE4m3Blk;
 }
 
 struct KvWriteParams {
@@ -40,6 +49,19 @@ struct KvWriteParams {
 
 cudaError_t launch_kv_write_quant(const KvWriteParams &p, int kv_dtype, cudaStream_t stream);
 
+struct KvWriteBlockParams {
+    uint8_t *k_cache, *v_cache;
+    float *k_scale_blk, *v_scale_blk;      // [blocks][Hkv]
+    const __half *k, *v;                   // [tokens][Hkv][128]
+    const int32_t *cu_seqlens_new;         // or null: q_len new tokens per sequence
+    const int32_t *block_table, *context_lens;
+    int max_blocks_per_seq, batch, max_new_len, q_len;
+    int num_kv_heads, num_blocks, block_size;
+    uint32_t *status;
+};
+
+cudaError_t launch_kv_write_block(const KvWriteBlockParams &p, int kv_dtype, cudaStream_t stream);
+
 struct DecodeParams {
     const uint8_t *k_cache, *v_cache;            // [blocks][Hkv][block_size][row bytes]
     const __half *k_new, *v_new;                 // nullable [batch][q_len][Hkv][128]: the
@@ -48,6 +70,7 @@ struct DecodeParams {
     const float *k_scale, *v_scale;              // FP8 formats: per KV head (or layer)
     int scale_stride;                            // 1: per KV head; 0: one per layer
     const uint16_t *k_scale_tok, *v_scale_tok;   // INT8: per (block, head, token)
+    const float *k_scale_blk, *v_scale_blk;      // block-scaled formats: [blocks][Hkv]
     int window;                                  // > 0: sliding window of keys
     const int32_t *query_pos;                    // nullable [batch][q_len]
     const __half *q;
@@ -68,6 +91,13 @@ struct DecodeParams {
     float scale_log2;    // softmax_scale * log2(e)
     float *ws_o;         // [row groups x Hkv][C][rows_per_cta][128] fp32, unnormalised
     float *ws_ml;        // [row groups x Hkv][C][rows_per_cta][2] fp32 (log2 max, sum)
+    // decode with weights: scores [batch][Hkv][score_keys][score_rows] (log2
+    // units; -inf for keys a row does not see and for padding rows) and the
+    // accumulator weights[b * weight_stride * Hkv + h * weight_stride + key]
+    float *scores;
+    float *weights;
+    long long weight_stride;
+    int score_keys, score_rows;
     uint32_t *status;
 };
 
@@ -79,12 +109,23 @@ struct DecodePlan {
     int split_min_blocks, split_gran;
     bool tc;                            // tensor-core kernel: all rows of a KV head in one CTA
     size_t workspace_bytes;
+    // decode with weights
+    size_t state_bytes;                 // the partial states in front of the scores
+    int score_keys, score_rows;
 };
 
 // Split plan for a decode shape on the current device (kv_dtype: kKvFp8 or
 // kKvInt8, whose kernels differ in registers and so in occupancy).
 bool decode_plan(int kv_dtype, int batch, int q_len, int num_q_heads, int num_kv_heads,
-                 int block_size, int max_context_len, DecodePlan *plan);
+                 int block_size, int max_context_len, bool weights, DecodePlan *plan);
+
+// Resident CTAs per SM of the split kernel that also stores the scores.
+int weights_split_occupancy(int kv_dtype, int nt, int block_size);
+
+// Decode that also adds every key's softmax weight to p.weights.
+cudaError_t launch_decode_weights(const DecodeParams &p, const DecodePlan &plan, int kv_dtype,
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                  cudaStream_t stream);
 
 // The tensor-core decode kernel (17..128 rows: all rows of a KV head in one
 // CTA, query rows on the MMA's M).
@@ -100,6 +141,7 @@ struct PrefillParams {
     const float *k_scale, *v_scale;
     int scale_stride;                            // 1: per KV head; 0: one per layer
     const uint16_t *k_scale_tok, *v_scale_tok;
+    const float *k_scale_blk, *v_scale_blk;      // block-scaled formats: [blocks][Hkv]
     int window;                                  // > 0: sliding window of keys
     const __half *q;
     __half *out;
@@ -143,11 +185,32 @@ struct CopyParams {
     int n;
     long long block_bytes;             // elements of one block (all heads), bytes
     int block_scales;                  // INT8 scales of one block (all heads)
+    const float *src_kb, *src_vb;      // block-scaled formats: [blocks][Hkv] (or null)
+    float *dst_kb, *dst_vb;
+    int num_kv_heads;
     int src_blocks, dst_blocks;
     uint32_t *status;
 };
 
 cudaError_t launch_copy_blocks(const CopyParams &p, cudaStream_t stream);
+
+struct EvictParams {
+    uint8_t *k_cache, *v_cache;
+    uint16_t *k_scale_tok, *v_scale_tok;   // INT8
+    float *k_scale_blk, *v_scale_blk;      // block-scaled formats
+    const float *weights;                  // [batch][Hkv][weight_stride]
+    long long weight_stride;
+    float *weights_out;                    // nullable [batch][Hkv][weight_out_stride]
+    long long weight_out_stride;
+    const int32_t *block_table, *context_lens, *dst_block_table;
+    int32_t *keep;                         // [batch][Hkv][budget]
+    int32_t *new_context_lens;
+    int max_blocks_per_seq, dst_max_blocks, block_size;
+    int batch, num_kv_heads, num_blocks, budget, sink, recent;
+    uint32_t *status;
+};
+
+cudaError_t launch_evict(const EvictParams &p, int kv_dtype, int block_size, cudaStream_t stream);
 
 int device_sm_count();
 

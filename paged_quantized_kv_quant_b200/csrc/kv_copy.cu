@@ -62,6 +62,12 @@ __global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const CopyParams 
         copy_run(reinterpret_cast<uint8_t *>(p.dst_vs) + (size_t)dst * sb,
                  reinterpret_cast<const uint8_t *>(p.src_vs) + (size_t)src * sb, sb);
     }
+    if (p.src_kb) {   // block-scaled formats: one K and one V scale per head
+        for (int h = threadIdx.x; h < p.num_kv_heads; h += kThreads) {
+            p.dst_kb[(size_t)dst * p.num_kv_heads + h] = p.src_kb[(size_t)src * p.num_kv_heads + h];
+            p.dst_vb[(size_t)dst * p.num_kv_heads + h] = p.src_vb[(size_t)src * p.num_kv_heads + h];
+        }
+    }
 }
 
 }  // namespace

@@ -29,6 +29,7 @@ struct CacheView {
     const uint16_t *ks, *vs;       // INT8: per-(block, head, token) fp16 scales
     int num_kv_heads, num_blocks;
     uint32_t *status;
+    const float *kb, *vb;          // block-scaled formats: scales [blocks][Hkv]
 };
 
 // A producer warp's window over one block-table row: entries [wbase,
@@ -112,6 +113,18 @@ __device__ __forceinline__ void copy_int8_scales(uint32_t kdst, uint32_t vdst, c
         const size_t y = ((size_t)phys * cv.num_kv_heads + h) * BS + (8 * q) % BS;
         cp_async_16((lane < nck ? kdst : vdst) + q * 16, (lane < nck ? cv.ks : cv.vs) + y);
     }
+}
+
+// Block-scaled formats: the K scales of nb blocks (at most 4) to dst, the V
+// scales to dst + 16, 4 bytes each.
+__device__ __forceinline__ void copy_block_scales(uint32_t dst, const CacheView &cv, int h,
+                                                  const BlockWindow &w, int blk0, int nb, int lane)
+{
+    const int i = lane >> 1, isv = lane & 1;
+    const int phys = w.id(blk0 + min(i, max(nb - 1, 0)), cv);   // all lanes
+    if (i < nb)
+        cp_async_4(dst + isv * 16 + i * 4,
+                   (isv ? cv.vb : cv.kb) + (size_t)phys * cv.num_kv_heads + h);
 }
 
 // FP16 rows (256 bytes) of `rows` keys (a multiple of 2) into [d half][row]

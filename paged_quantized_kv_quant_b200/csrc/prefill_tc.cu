@@ -35,6 +35,11 @@
 //               tensor core runs one group's products while the other group's
 //               softmax runs.
 //
+// Block-scaled formats (a K and a V scale per block and KV head): the dequant
+// warps hand the softmax each key's score factor (K scale) and log2 of its V
+// scale, and the softmax takes p' = 2^(s + log2 vs - M), l += p' / vs: codes
+// enter the tensor core exactly and no V element is multiplied.
+//
 // FP16 caches need no conversion: the TMA warp copies each block's two
 // 128-byte row halves straight into a K/V buffer, and the dequant warps only
 // clear rows past the context.  With a sliding window w ("1Cat-LLM" README,
@@ -76,7 +81,10 @@ constexpr int kOffCodes = kOffKV + kKVBufs * kKVBuf;      // stages x (K 8K, V 8
 constexpr int kCodeStage = 16384;
 constexpr int kOffScl = kOffCodes + kCodeStages * kCodeStage;   // stages x (K 64, V 64) halves
 constexpr int kOffKsf = kOffScl + kCodeStages * 256;            // bufs x 64 fp32 K factors
-constexpr int kOffBars = kOffKsf + kKVBufs * 64 * 4;
+// block-scaled formats: bufs x 64 fp32 log2 V scales, bufs x 4 fp32 1 / V scale (16 keys each)
+constexpr int kOffLvf = kOffKsf + kKVBufs * 64 * 4;
+constexpr int kOffIvf = kOffLvf + kKVBufs * 64 * 4;
+constexpr int kOffBars = kOffIvf + kKVBufs * 4 * 4;
 constexpr int kNumBars = 1 + 2 * kCodeStages + 3 * kKVBufs + 3 * 2 + 1;
 constexpr int kOffTaddr = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffTaddr + 16;
@@ -129,7 +137,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32
 template <int KVT>
 __device__ __forceinline__ void cvt4(uint32_t x, uint32_t &lo, uint32_t &hi)
 {
-    if constexpr (KVT == kKvFp8)
+    if constexpr (KVT == kKvFp8 || KVT == kKvE4m3Blk)
         e4m3x4_to_half2x2(x, lo, hi);
     else if constexpr (KVT == kKvE5m2)
         e5m2x4_to_half2x2(x, lo, hi);
@@ -232,7 +240,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // tile's barrier once its own copies have landed.  The tiles up to
         // kPrefetchTiles past the one being loaded are first fetched into L2.
         const CacheView cv{p.k_cache, p.v_cache, p.k_scale_tok, p.v_scale_tok, p.num_kv_heads,
-                           p.num_blocks, p.status};
+                           p.num_blocks, p.status, p.k_scale_blk, p.v_scale_blk};
         BlockWindow w;
         // every index stays inside the table row, even for a context longer
         // than the row can address (a caller error: those keys read block 0)
@@ -263,6 +271,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const uint32_t sd = sbase + kOffScl + s * 256;
                     copy_int8_scales<BS>(sd, sd + 128, cv, h, w, blk0, nb, lane);
                 }
+                if constexpr (kv_has_block_scale(KVT))
+                    copy_block_scales(sbase + kOffScl + s * 256, cv, h, w, blk0, nb, lane);
                 cp_async_mbar_arrive(&bars.code_full[s]);
             }
             if (j + 1 < ntiles)
@@ -446,6 +456,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 ksf[row] =
                     key0 + row < ctx ? kfac * __half2float(__ushort_as_half(scl[row])) : 0.0f;
             }
+            if constexpr (kv_has_block_scale(KVT)) {
+                // scale 0: every code of the block is 0, any factor serves
+                const float *sb = reinterpret_cast<const float *>(scl) + row / BS;
+                const bool live = key0 + row < ctx;
+                const float vs = live && sb[4] > 0.0f ? sb[4] : 1.0f;
+                reinterpret_cast<float *>(smem + kOffKsf)[bj * 64 + row] = live ? kfac * sb[0] : 0.0f;
+                reinterpret_cast<float *>(smem + kOffLvf)[bj * 64 + row] = log2f(vs);
+                if ((row & 15) == 0)
+                    reinterpret_cast<float *>(smem + kOffIvf)[bj * 4 + row / 16] = __frcp_rn(vs);
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -499,7 +519,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 ok = false;
                 break;
             }
-            if constexpr (KVT == kKvInt8) {
+            if constexpr (KVT == kKvInt8 || kv_has_block_scale(KVT)) {
                 // the per-key factors below were written by the dequant warps
                 if (!warp_wait(&bars.kv_full[j % kKVBufs], (j / kKVBufs) & 1, p.status)) {
                     ok = false;
@@ -519,7 +539,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             }
 
             const int key0 = (jbase + j) * kKT;
-            if constexpr (KVT != kKvInt8) {
+            if constexpr (kv_has_block_scale(KVT)) {
+                const float *ksf =
+                    reinterpret_cast<const float *>(smem + kOffKsf) + (j % kKVBufs) * 64;
+                const float *lvf =
+                    reinterpret_cast<const float *>(smem + kOffLvf) + (j % kKVBufs) * 64;
+#pragma unroll
+                for (int c = 0; c < kKT; c += 2) {
+                    const float2 r2 = __ffma2_rn(make_float2(v[c], v[c + 1]),
+                                                 make_float2(ksf[c], ksf[c + 1]),
+                                                 make_float2(lvf[c], lvf[c + 1]));
+                    v[c] = r2.x, v[c + 1] = r2.y;
+                }
+            } else if constexpr (KVT != kKvInt8) {
                 const float2 f2 = make_float2(kfac, kfac);
 #pragma unroll
                 for (int c = 0; c < kKT; c += 2) {
@@ -583,12 +615,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             for (int c = 0; c < kKT; c += 2) {
                 const float2 d = __fadd2_rn(make_float2(v[c], v[c + 1]), nmu);
                 const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-                acc[(c >> 1) & 3] = __fadd2_rn(acc[(c >> 1) & 3], e);
+                // (block-scaled: one sum for each 16 keys, which share a V scale)
+                const int ai = kv_has_block_scale(KVT) ? c >> 4 : (c >> 1) & 3;
+                acc[ai] = __fadd2_rn(acc[ai], e);
                 pk[c / 2] = pack_half2(e.x, e.y);
             }
-            const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-            const float2 a = __fadd2_rn(a01, a23);
-            l += a.x + a.y;
+            if constexpr (kv_has_block_scale(KVT)) {
+                const float *ivf = reinterpret_cast<const float *>(smem + kOffIvf) + (j % kKVBufs) * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    l = fmaf(acc[i].x + acc[i].y, ivf[i], l);
+            } else {
+                const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+                const float2 a = __fadd2_rn(a01, a23);
+                l += a.x + a.y;
+            }
             // P row over the first 32 S columns (the A operand of P V)
             tmem_st32(tl + kTmS, pk);
             tmem_st_wait();
@@ -668,6 +709,8 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, int kv_dtype, const CUtens
         PKVQ_TC_CASE(kKvInt8, 16) PKVQ_TC_CASE(kKvInt8, 32) PKVQ_TC_CASE(kKvInt8, 64)
         PKVQ_TC_CASE(kKvE5m2, 16) PKVQ_TC_CASE(kKvE5m2, 32) PKVQ_TC_CASE(kKvE5m2, 64)
         PKVQ_TC_CASE(kKvFp16, 16) PKVQ_TC_CASE(kKvFp16, 32) PKVQ_TC_CASE(kKvFp16, 64)
+        PKVQ_TC_CASE(kKvInt8Blk, 16) PKVQ_TC_CASE(kKvInt8Blk, 32) PKVQ_TC_CASE(kKvInt8Blk, 64)
+        PKVQ_TC_CASE(kKvE4m3Blk, 16) PKVQ_TC_CASE(kKvE4m3Blk, 32) PKVQ_TC_CASE(kKvE4m3Blk, 64)
 #undef PKVQ_TC_CASE
     default: return cudaErrorInvalidValue;
     }

@@ -139,14 +139,14 @@ __device__ __forceinline__ uint32_t int8_code(uint32_t rbits)
 }
 
 // 8 fp16 values -> 8 INT8 codes clamp(rint(x / s), -127, 127) (s == 0 ->
-// codes 0).  |x / s| stays near 127 at most, far inside rint_bits' range.
-__device__ __forceinline__ uint2 quant_int8_8(const uint4 &x, uint16_t scale_bits)
+// codes 0).  |x / s| stays near 127 at most, far inside rint_bits' range; s is
+// an fp16 value or absmax / 127 of fp16 values, whose reciprocal is normal.
+__device__ __forceinline__ uint2 quant_int8_8(const uint4 &x, float s)
 {
-    const float s = __half2float(__ushort_as_half(scale_bits));
     if (s == 0.0f)
         return make_uint2(0u, 0u);
     float r_lo, r_hi;
-    recip_bracket(s, r_lo, r_hi);   // an fp16 scale's reciprocal is always normal
+    recip_bracket(s, r_lo, r_hi);
     const __half2 *h = reinterpret_cast<const __half2 *>(&x);
     uint32_t w[2] = {0u, 0u};
     bool same = true;
@@ -169,6 +169,68 @@ __device__ __forceinline__ uint2 quant_int8_8(const uint4 &x, uint16_t scale_bit
         }
     }
     return make_uint2(w[0], w[1]);
+}
+
+// --- block-scaled formats: one fp32 scale per (block, KV head) ---
+
+// Largest code magnitude: a block's scale is absmax / this.
+template <int KVT>
+__device__ __forceinline__ constexpr float block_code_max()
+{
+    return KVT == kKvInt8Blk ? 127.0f : 448.0f;
+}
+
+// +-inf -> +-65504 and NaN -> 0, so that one such input neither voids a
+// block's scale nor reaches the codes (a half is one of them iff its exponent
+// is all ones: adding 0x0400 to the magnitude then carries into bit 15).
+__device__ __forceinline__ uint4 finite8(uint4 x)
+{
+    const uint32_t m = 0x7fff7fffu, k = 0x04000400u;
+    const uint32_t t = ((x.x & m) + k) | ((x.y & m) + k) | ((x.z & m) + k) | ((x.w & m) + k);
+    if (t & 0x80008000u) {
+        uint16_t *h = reinterpret_cast<uint16_t *>(&x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((h[i] & 0x7c00u) == 0x7c00u)
+                h[i] = (h[i] & 0x03ffu) ? 0u : (uint16_t)((h[i] & 0x8000u) | 0x7bffu);
+    }
+    return x;
+}
+
+// 8 finite fp16 values -> 8 codes of x / s (s == 0 -> codes 0).
+template <int KVT>
+__device__ __forceinline__ uint2 quant_block_8(const uint4 &x, float s)
+{
+    if constexpr (KVT == kKvInt8Blk) {
+        return quant_int8_8(x, s);
+    } else {
+        float lo, hi;
+        const bool fast = recip_bracket(s, lo, hi);
+        return quant_fp8_8<kKvFp8>(x, s, lo, hi, fast);
+    }
+}
+
+// 4 codes of a block whose scale grew: the codes of RN(value * ratio), ratio =
+// RN(old scale / new scale) < 1.
+template <int KVT>
+__device__ __forceinline__ uint32_t requant_block_4(uint32_t codes, float ratio)
+{
+    if constexpr (KVT == kKvInt8Blk) {
+        uint32_t r = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v = (float)(int8_t)(codes >> (8 * i));
+            r |= int8_code(rint_bits(__fmul_rn(v, ratio))) << (8 * i);
+        }
+        return r;
+    } else {
+        uint32_t lo, hi;
+        e4m3x4_to_half2x2(codes, lo, hi);
+        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
+        return quant_fp8x2<kKvFp8>(__fmul_rn(a.x, ratio), __fmul_rn(a.y, ratio)) |
+               (quant_fp8x2<kKvFp8>(__fmul_rn(b.x, ratio), __fmul_rn(b.y, ratio)) << 16);
+    }
 }
 
 // One thread's 8 elements (16-byte piece `sub` of 16) of a (token, KV head)
@@ -195,7 +257,7 @@ __device__ __forceinline__ void quant_store_piece(uint8_t *cache, uint16_t *scal
             c = quant_fp8_8<KVT>(x, sc, lo, hi, fast);
         } else {
             const uint16_t sb = int8_row_scale(absmax8(x));
-            c = quant_int8_8(x, sb);
+            c = quant_int8_8(x, __half2float(__ushort_as_half(sb)));
             if (write && sub == 0)
                 scale_tok[drow] = sb;
         }
