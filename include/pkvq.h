@@ -312,6 +312,46 @@ PKVQ_API pkvq_status pkvq_paged_attn_decode_append(const pkvq_cache *cache, cons
                                    float softmax_scale, const pkvq_attn_opts *opts,
                                    void *workspace, size_t workspace_bytes, void *stream);
 
+/* Element types of pkvq_prompt_attn. */
+typedef enum { PKVQ_FP16 = 0, PKVQ_BF16 = 1 } pkvq_dtype;
+
+/* Queries, keys and values of packed prompts, as the projections leave them:
+ * row (token, head) is head_dim contiguous elements at token * token_stride +
+ * head * head_stride (elements; multiples of 8, at least head_dim), so slices
+ * of one fused projection serve.  Pointers 16-byte aligned. */
+typedef struct {
+    int32_t dtype;          /* pkvq_dtype of q, k, v and out */
+    int32_t head_dim;       /* must be 128 */
+    int32_t num_q_heads;    /* a multiple of num_kv_heads, at most 128 times it */
+    int32_t num_kv_heads;
+    int64_t total;          /* rows (tokens) of q, k and v */
+    const void *q, *k, *v;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+} pkvq_prompt;
+
+/*
+ * Causal attention over whole prompts of different lengths, packed: token i
+ * of a sequence attends to keys max(0, i - w + 1) .. i of the same sequence
+ * (w = sliding_window; 0: keys 0 .. i), at full precision, before or without
+ * reading them back from a cache.
+ *   out         [total][num_q_heads][head_dim], contiguous, of t->dtype
+ *   lse_out     nullable fp32 [total][num_q_heads]: natural-log sum-exp of the
+ *               scaled scores
+ *   cu_seqlens  int32 [batch + 1], cu[0] = 0, nondecreasing, cu[batch] <= total;
+ *               rows at or behind cu[batch] are left as they were
+ *   max_len     host-side upper bound of the sequences' lengths (tokens behind
+ *               it get no output)
+ * Sequences do not touch each other, whatever their neighbours hold.  Inside a
+ * sequence V must be finite (a masked weight of 0 times infinity is NaN).
+ * batch and num_kv_heads at most 65535; batch == 0, max_len == 0 or total == 0
+ * is a no-op.
+ */
+PKVQ_API pkvq_status pkvq_prompt_attn(const pkvq_prompt *t, void *out, float *lse_out,
+                                   const int32_t *cu_seqlens, int32_t batch, int32_t max_len,
+                                   float softmax_scale, int32_t sliding_window, void *stream);
+
 /* Workspace bytes of pkvq_paged_attn_decode_weights (0 on invalid arguments):
  * the split-KV partial states and the fp32 score of every (query row, key). */
 PKVQ_API size_t pkvq_decode_weights_workspace_bytes(int32_t batch, int32_t q_len,

@@ -11,6 +11,7 @@ Entry points (same names as the C ABI, without the ``pkvq_`` prefix):
   kv_write_quant, kv_write_block_quant (block-scaled formats),
   decode_workspace_bytes, paged_attn_decode (with the _ex options as keyword
   arguments: sliding_window, query_pos), paged_attn_decode_append,
+  prompt_attn (whole packed prompts, K and V as projected),
   paged_attn_decode_weights and decode_weights_workspace_bytes (decode that
   accumulates every key's attention weight), kv_evict (eviction by those
   weights), paged_attn_prefill (sliding_window), merge_attn_states,
@@ -46,6 +47,7 @@ EXPORTED = (
     "pkvq_decode_weights_workspace_bytes",
     "pkvq_paged_attn_decode_weights",
     "pkvq_kv_evict",
+    "pkvq_prompt_attn",
     "pkvq_decode_workspace_bytes",
     "pkvq_paged_attn_decode_append",
     "pkvq_paged_attn_decode",
@@ -95,6 +97,25 @@ class CacheStruct(ctypes.Structure):
     ]
 
 
+class PromptStruct(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("total", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
 class AttnOpts(ctypes.Structure):
     _fields_ = [
         ("sliding_window", ctypes.c_int32),
@@ -129,6 +150,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.pkvq_kv_evict.restype = I32
     lib.pkvq_kv_evict.argtypes = [P, P, ctypes.c_int64, P, I32, P, I32, I32, I32, I32, P, I32,
                                   P, P, P, ctypes.c_int64, P]
+    lib.pkvq_prompt_attn.restype = I32
+    lib.pkvq_prompt_attn.argtypes = [P, P, P, P, I32, I32, ctypes.c_float, I32, P]
     lib.pkvq_decode_workspace_bytes.restype = SZ
     lib.pkvq_decode_workspace_bytes.argtypes = [I32, I32, I32, I32, P]
     lib.pkvq_paged_attn_decode.restype = I32
@@ -601,6 +624,58 @@ def paged_attn_prefill(cache: PagedKVCache, q: torch.Tensor, cu_seqlens_q: torch
             _ptr(block_table), int(block_table.shape[1]), _ptr(context_lens), B, int(max_q_len),
             Hq, float(softmax_scale), None if opts is None else ctypes.byref(opts), None, 0,
             _stream(stream)), "paged_attn_prefill")
+    return out
+
+
+_PROMPT_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                max_len: int, softmax_scale: float, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, stream=None,
+                sliding_window: int = 0) -> torch.Tensor:
+    """Causal attention over packed whole prompts: q [T][Hq][D], k and v
+    [T][Hkv][D], fp16 or bf16, the rows of sequence b from cu_seqlens[b] to
+    cu_seqlens[b + 1] (int32 [B + 1]) -> out [T][Hq][D] (lse fp32 [T][Hq]).  The
+    last dimension is contiguous; token and head strides may be those of
+    slices of one fused projection (multiples of 8 elements)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dtype = _PROMPT_DTYPES.get(q.dtype)
+    if dtype is None:
+        raise TypeError(f"q must be fp16 or bf16, got {q.dtype}")
+    dev = q.get_device()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype != q.dtype or t.get_device() != dev:
+            raise TypeError(f"{name} must be {q.dtype} on cuda:{dev}")
+        if t.dim() != 3 or t.stride(2) != 1:
+            raise ValueError(f"{name} must have 3 dims, the last one contiguous")
+        if t.shape[0] != q.shape[0] or t.shape[2] != q.shape[2]:
+            raise ValueError(f"{name} must have q's tokens and head_dim")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    T, Hq, D = q.shape
+    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
+    if cu_seqlens.shape[0] < 1 or cu_seqlens.get_device() != dev:
+        raise ValueError(f"cu_seqlens must hold batch + 1 entries on cuda:{dev}")
+    (qt, qh, _), (kt, kh, _), (vt, vh, _) = q.stride(), k.stride(), v.stride()
+    # (a dimension of one element may carry any stride)
+    if Hq == 1:
+        qh = D
+    if k.shape[1] == 1:
+        kh = vh = D
+    if T == 1:
+        qt, kt, vt = Hq * D, k.shape[1] * D, k.shape[1] * D
+    ps = PromptStruct(dtype, D, Hq, k.shape[1], T, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                      qt, qh, kt, kh, vt, vh)
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        _args(dev, out=(out, q.dtype, (T, Hq, D)), lse=(lse, torch.float32, (T, Hq)))
+        _check(_lib().pkvq_prompt_attn(
+            ctypes.byref(ps), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
+            int(cu_seqlens.shape[0]) - 1, int(max_len), float(softmax_scale),
+            int(sliding_window), _stream(stream, q.device)), "prompt_attn")
     return out
 
 

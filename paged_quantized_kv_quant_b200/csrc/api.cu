@@ -140,6 +140,23 @@ bool make_cache_tensor_map(CUtensorMap *map, const void *base, uint64_t rows, in
     return r == CUDA_SUCCESS;
 }
 
+bool make_rows_tensor_map(CUtensorMap *map, const void *base, bool bf16, int64_t tokens,
+                          int heads, int64_t token_stride, int64_t head_stride, int box_heads,
+                          int box_tokens)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_sm_count()
 {
     static int counts[kMaxDevices] = {};
@@ -592,6 +609,65 @@ pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights, int64_t
         return PKVQ_ERR_CUDA;
     return from_cuda(launch_evict(p, cache->dtype, cache->block_size,
                                   static_cast<cudaStream_t>(stream)));
+}
+
+pkvq_status pkvq_prompt_attn(const pkvq_prompt *t, void *out, float *lse_out,
+                             const int32_t *cu_seqlens, int32_t batch, int32_t max_len,
+                             float softmax_scale, int32_t sliding_window, void *stream)
+{
+    if (!t || batch < 0 || max_len < 0 || t->total < 0 || t->num_q_heads <= 0 ||
+        t->num_kv_heads <= 0 || t->num_q_heads % t->num_kv_heads || sliding_window < 0 ||
+        !isfinite(softmax_scale))
+        return PKVQ_ERR_INVALID_ARG;
+    const int group = t->num_q_heads / t->num_kv_heads;
+    if (t->head_dim != kHeadDim || (t->dtype != PKVQ_FP16 && t->dtype != PKVQ_BF16) ||
+        group > 128 || batch > kMaxGridYZ || t->num_kv_heads > kMaxGridYZ)
+        return PKVQ_ERR_UNSUPPORTED;
+    if (batch == 0 || max_len == 0 || t->total == 0)
+        return PKVQ_OK;
+    if (!t->q || !t->k || !t->v || !out || !cu_seqlens)
+        return PKVQ_ERR_INVALID_ARG;
+    const void *base[3] = {t->q, t->k, t->v};
+    const int64_t ts[3] = {t->q_token_stride, t->k_token_stride, t->v_token_stride};
+    const int64_t hs[3] = {t->q_head_stride, t->k_head_stride, t->v_head_stride};
+    if (!aligned16(out))
+        return PKVQ_ERR_MISALIGNED;
+    for (int i = 0; i < 3; ++i) {
+        // rows are 128 contiguous elements; a stride of at most 2^40 bytes
+        if (ts[i] < kHeadDim || hs[i] < kHeadDim || ts[i] >= (1LL << 38) || hs[i] >= (1LL << 38))
+            return PKVQ_ERR_INVALID_ARG;
+        if (!aligned16(base[i]) || ts[i] % 8 || hs[i] % 8)
+            return PKVQ_ERR_MISALIGNED;
+    }
+    const bool bf16 = t->dtype == PKVQ_BF16;
+    PromptParams p{};
+    p.tokens_per_tile = 128 / group;
+    CUtensorMap m[3];
+    for (int i = 0; i < 3; ++i)
+        if (!make_rows_tensor_map(&m[i], base[i], bf16, t->total,
+                                  i == 0 ? t->num_q_heads : t->num_kv_heads, ts[i], hs[i],
+                                  i == 0 ? group : 1, i == 0 ? p.tokens_per_tile : 128))
+            return PKVQ_ERR_CUDA;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse_out;
+    p.cu_seqlens = cu_seqlens;
+    p.total = t->total;
+    p.batch = batch;
+    p.num_q_heads = t->num_q_heads;
+    p.num_kv_heads = t->num_kv_heads;
+    p.group = group;
+    p.q_tiles = (int)(((long long)max_len + p.tokens_per_tile - 1) / p.tokens_per_tile);
+    p.window = sliding_window;
+    // a scale of 0 becomes one whose scores all round to 0, so that a masked
+    // score (-inf) stays one
+    const float s = softmax_scale == 0.0f ? 1e-30f : softmax_scale;
+    p.scale_log2 = fabsf(s) * kLog2e;
+    p.negate = s < 0.0f;
+    p.bf16 = bf16;
+    p.status = status_ptr();
+    if (!p.status)
+        return PKVQ_ERR_CUDA;
+    return from_cuda(launch_prompt_attn(p, m[0], m[1], m[2], static_cast<cudaStream_t>(stream)));
 }
 
 pkvq_status pkvq_paged_attn_prefill(const pkvq_cache *cache, const void *q, void *out,

@@ -194,6 +194,30 @@ struct CopyParams {
 
 cudaError_t launch_copy_blocks(const CopyParams &p, cudaStream_t stream);
 
+struct PromptParams {
+    uint16_t *out;                   // fp16 or bf16 [total][Hq][128]
+    float *lse;
+    const int32_t *cu_seqlens;
+    long long total;                 // rows of q, k, v and out
+    int batch, num_q_heads, num_kv_heads, group;
+    int tokens_per_tile, q_tiles;    // 128 / group; ceil(max_len / tokens_per_tile)
+    int window;
+    float scale_log2;                // |softmax_scale| * log2(e), > 0
+    bool negate;                     // softmax_scale < 0
+    bool bf16;
+    uint32_t *status;
+};
+
+cudaError_t launch_prompt_attn(const PromptParams &p, const CUtensorMap &qmap,
+                               const CUtensorMap &kmap, const CUtensorMap &vmap,
+                               cudaStream_t stream);
+
+// 3-D map of 16-bit rows [tokens][heads][128] with the given strides (elements):
+// boxes of 64 d x box_heads x box_tokens, 128-byte swizzle, zeros outside.
+bool make_rows_tensor_map(CUtensorMap *map, const void *base, bool bf16, int64_t tokens,
+                          int heads, int64_t token_stride, int64_t head_stride, int box_heads,
+                          int box_tokens);
+
 struct EvictParams {
     uint8_t *k_cache, *v_cache;
     uint16_t *k_scale_tok, *v_scale_tok;   // INT8

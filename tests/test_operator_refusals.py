@@ -134,3 +134,38 @@ def test_python_checks_before_any_call():
         pk.kv_write_block_quant(c, torch.zeros((1, 2, 128)), torch.zeros((1, 2, 128)), i32, i32[None], i32[:1], 1)
     with pytest.raises(ValueError):
         pk.kv_evict(c, torch.zeros((1, 2, 16)), i32[None], i32[:1], i32[None], 4)
+
+
+def prompt(lib, out=0x40000, cu=0x50000, B=2, mx=64, scale=0.088, window=0, **kw):
+    a = dict(dtype=0, head_dim=128, num_q_heads=8, num_kv_heads=2, total=100, q=0x10000, k=0x20000, v=0x30000,
+             q_token_stride=1024, q_head_stride=128, k_token_stride=256, k_head_stride=128,
+             v_token_stride=256, v_head_stride=128)
+    a.update(kw)
+    s = pk.PromptStruct(**a)
+    return lib.pkvq_prompt_attn(ctypes.byref(s), P(out), None, P(cu), B, mx, ctypes.c_float(scale), window, None)
+
+
+def test_prompt_refusals(lib):
+    assert lib.pkvq_prompt_attn(None, P(16), None, P(16), 1, 1, ctypes.c_float(1), 0, None) == INVALID
+    assert prompt(lib, dtype=2) == UNSUPPORTED
+    assert prompt(lib, head_dim=64) == UNSUPPORTED
+    assert prompt(lib, num_q_heads=7) == INVALID
+    assert prompt(lib, num_q_heads=258) == UNSUPPORTED           # group 129
+    assert prompt(lib, B=65536) == UNSUPPORTED
+    assert prompt(lib, B=-1) == INVALID
+    assert prompt(lib, mx=-1) == INVALID
+    assert prompt(lib, total=-1) == INVALID
+    assert prompt(lib, window=-1) == INVALID
+    assert prompt(lib, scale=float("inf")) == INVALID
+    for name in ("q", "k", "v"):
+        assert prompt(lib, **{name: None}) == INVALID
+        assert prompt(lib, **{name: 0x10008}) == MISALIGNED
+        assert prompt(lib, **{name + "_token_stride": 1028}) == MISALIGNED
+        assert prompt(lib, **{name + "_head_stride": 132}) == MISALIGNED
+        assert prompt(lib, **{name + "_head_stride": 0}) == INVALID
+        assert prompt(lib, **{name + "_token_stride": 1 << 40}) == INVALID
+    assert prompt(lib, out=None) == INVALID
+    assert prompt(lib, out=0x40008) == MISALIGNED
+    assert prompt(lib, cu=None) == INVALID
+    for kw in (dict(B=0), dict(mx=0), dict(total=0)):
+        assert prompt(lib, **kw) == OK
