@@ -255,6 +255,17 @@ pkvq_status pkvq_kv_write_quant(const pkvq_cache *cache, const void *k, const vo
 
 namespace {
 
+// Two warps for each 16 rows of every block and head that the call may touch,
+// within CUDA's limit of blocks in a grid.
+bool block_write_grid_fits(const pkvq_cache *cache, int32_t batch, int32_t max_new_len)
+{
+    const long long touched =
+        ((long long)max_new_len + cache->block_size - 2) / cache->block_size + 1;
+    const long long units = touched * batch;
+    return units < (1LL << 31) && cache->num_kv_heads <= kMaxGridYZ &&
+           units * cache->num_kv_heads * (cache->block_size / 16) < (1LL << 33) - 8;
+}
+
 KvWriteBlockParams block_write_params(const pkvq_cache *cache, const void *k, const void *v,
                                       const int32_t *cu_seqlens_new, const int32_t *block_table,
                                       int32_t max_blocks_per_seq, const int32_t *context_lens,
@@ -300,9 +311,8 @@ pkvq_status pkvq_kv_write_block_quant(const pkvq_cache *cache, const void *k, co
         return PKVQ_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v))
         return PKVQ_ERR_MISALIGNED;
-    if ((((long long)max_new_len + cache->block_size - 2) / cache->block_size + 1) * batch >=
-            (1LL << 31) || cache->num_kv_heads > kMaxGridYZ)
-        return PKVQ_ERR_UNSUPPORTED;   // the launch grid
+    if (!block_write_grid_fits(cache, batch, max_new_len))
+        return PKVQ_ERR_UNSUPPORTED;
     uint32_t *status = status_ptr();
     if (!status)
         return PKVQ_ERR_CUDA;
@@ -457,7 +467,7 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
         if (kv_has_block_scale(cache->dtype)) {
             // a block's scale follows from all its new tokens: the block
             // write kernel runs just before
-            if (cache->num_kv_heads > kMaxGridYZ || (2LL + q_len / 16) * batch >= (1LL << 31))
+            if (!block_write_grid_fits(cache, batch, q_len))
                 return PKVQ_ERR_UNSUPPORTED;
             const cudaError_t e = launch_kv_write_block(
                 block_write_params(cache, k_new, v_new, nullptr, block_table, max_blocks_per_seq,
