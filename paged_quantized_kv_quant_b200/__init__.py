@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -221,13 +222,16 @@ def _check(status: int, what: str) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream, device=None) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream, device: Optional[int] = None) -> int:
+    """Raw stream: the given one, or the current one of a CUDA device index."""
+    if stream is not None:
+        return stream.cuda_stream
+    if device is None:
+        device = torch._C._cuda_getDevice()
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 _SAME_DEVICE = contextlib.nullcontext()
@@ -238,32 +242,49 @@ def _on(t: torch.Tensor, stream=None):
     launches go there, and what the call allocates belongs to that stream."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if t.get_device() == torch.cuda.current_device():
+    if t.get_device() == torch._C._cuda_getDevice():
         return _SAME_DEVICE
     return torch.cuda.device(t.device)
 
 
-def _batch(B: int, q: torch.Tensor, out, lse, block_table, context_lens) -> None:
-    """The shapes that go with a batch of B sequences and the queries q."""
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is not None and lse.shape != q.shape[:-1]:
-        raise ValueError("lse must have q's shape without head_dim")
-    if block_table.shape[0] != B or context_lens.shape[0] != B:
-        raise ValueError(f"block_table and context_lens must have {B} rows")
+def _arg(name: str, t, dtype, shape: tuple, device: int) -> Optional[int]:
+    """Address of a tensor of exactly this dtype and shape, contiguous, on CUDA
+    device `device`; None for None."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{device}")
 
 
-def _args(device: int, **tensors) -> None:
-    """Checks (tensor, dtype, shape) triples: dtype, exact shape, contiguous, on
-    CUDA device `device`.  None tensors are skipped."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        _need(t, dtype, name)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be on cuda:{device}")
+def _cols(name: str, t) -> int:
+    """Columns of a 2-D tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape[1]
+
+
+def _rows(name: str, t) -> int:
+    """Entries of a 1-D tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D tensor")
+    return t.shape[0]
+
+
+def _scratch(workspace: Optional[torch.Tensor], device: int):
+    """(address, bytes) of a caller's workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _need(t: torch.Tensor, dtype, name: str, ndim: Optional[int] = None,
@@ -344,6 +365,23 @@ class PagedKVCache:
         return self.k_cache.shape[3] // elem_bytes(self.dtype)
 
     def struct(self, device_ok: bool = False) -> CacheStruct:
+        """The cache as the C ABI sees it.  Kept with the object: the tensors are
+        checked again when one of them, or its address, has changed."""
+        tensors = (self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.k_scale_tok,
+                   self.v_scale_tok, self.k_scale_blk, self.v_scale_blk)
+        seen = [None if t is None else t.data_ptr() for t in tensors]
+        kept = self.__dict__.get("_kept")
+        if kept is not None and not device_ok:
+            old, addresses, dtype, per_layer, cs = kept
+            if (addresses == seen and dtype == self.dtype and per_layer == self.scale_per_layer
+                    and all(map(operator.is_, old, tensors))):
+                return cs
+        cs = self._struct(device_ok)
+        if not device_ok:
+            self.__dict__["_kept"] = (tensors, seen, self.dtype, self.scale_per_layer, cs)
+        return cs
+
+    def _struct(self, device_ok: bool) -> CacheStruct:
         for name in ("k_cache", "v_cache"):
             _need(getattr(self, name), torch.uint8, name, 4, host_ok=device_ok)
         if self.dtype in _FP8_FORMATS:
@@ -359,8 +397,15 @@ class PagedKVCache:
                 _need(t, torch.float32, name, 2, host_ok=device_ok)
                 if t.shape != self.k_cache.shape[:2]:
                     raise ValueError(f"{name} must be [num_blocks][num_kv_heads]")
-            if self.v_cache.shape != self.k_cache.shape:
-                raise ValueError("k_cache and v_cache must have the same shape")
+        if self.v_cache.shape != self.k_cache.shape:
+            raise ValueError("k_cache and v_cache must have the same shape")
+        if self.dtype == KV_INT8 and not (self.k_scale_tok.shape == self.v_scale_tok.shape ==
+                                          self.k_cache.shape[:3]):
+            raise ValueError("per-token scales must be [num_blocks][num_kv_heads][block_size]")
+        if not device_ok and len({t.get_device() for t in (
+                self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.k_scale_tok,
+                self.v_scale_tok, self.k_scale_blk, self.v_scale_blk) if t is not None}) > 1:
+            raise ValueError("the cache's tensors must be on one device")
         nb, hkv, bs, rb = self.k_cache.shape
         return CacheStruct(self.dtype, nb, bs, hkv, rb // elem_bytes(self.dtype),
                            self.k_cache.data_ptr(), self.v_cache.data_ptr(),
@@ -392,19 +437,17 @@ def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
     every sequence b (packed), into a block-scaled cache; context_lens counts
     them.  A block's scale covers the tokens written to it: it grows when a
     louder token arrives, and the block's older codes are rounded again."""
-    B = int(context_lens.shape[0])
     cs = cache.struct()
     dev = cache.k_cache.get_device()
-    _args(dev, k=(k, torch.float16, (k.shape[0], cache.num_kv_heads, cache.head_dim)),
-          v=(v, torch.float16, tuple(k.shape)),
-          cu_seqlens_new=(cu_seqlens_new, torch.int32, (B + 1,)),
-          block_table=(block_table, torch.int32, (B, block_table.shape[-1])),
-          context_lens=(context_lens, torch.int32, (B,)))
+    B, cols = _rows("context_lens", context_lens), _cols("block_table", block_table)
+    rows = (k.shape[0], cs.num_kv_heads, cs.head_dim)
+    args = (_arg("k", k, torch.float16, rows, dev), _arg("v", v, torch.float16, rows, dev),
+            _arg("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev),
+            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_new_len))
     with _on(k, stream):
-        _check(_lib().pkvq_kv_write_block_quant(
-            ctypes.byref(cs), _ptr(k), _ptr(v), _ptr(cu_seqlens_new), _ptr(block_table),
-            int(block_table.shape[1]), _ptr(context_lens), B, int(max_new_len),
-            _stream(stream, k.device)), "kv_write_block_quant")
+        _check(_lib().pkvq_kv_write_block_quant(ctypes.byref(cs), *args, _stream(stream, dev)),
+               "kv_write_block_quant")
 
 
 def decode_workspace_bytes(cache: PagedKVCache, batch: int, q_len: int, num_q_heads: int,
@@ -420,6 +463,14 @@ def _opts(sliding_window: int, query_pos: Optional[torch.Tensor]):
     return AttnOpts(int(sliding_window), None if query_pos is None else query_pos.data_ptr())
 
 
+def _queries(q: torch.Tensor, cs: CacheStruct):
+    """(batch, q_len, query heads, shape) of decode queries for a cache."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != cs.head_dim:
+        raise ValueError(f"q must be [batch][q_len][num_q_heads][{cs.head_dim}]")
+    shape = tuple(q.shape)
+    return shape[0], shape[1], shape[2], shape
+
+
 def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Tensor,
                       context_lens: torch.Tensor, max_context_len: int, softmax_scale: float,
                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -429,34 +480,28 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
     """q fp16 [B][q_len][Hq][D] -> out fp16 [B][q_len][Hq][D] (lse fp32 [B][q_len][Hq]).
     sliding_window > 0 limits every query to its last `sliding_window` keys;
     query_pos (int32 [B][q_len]) gives each query's position among the keys."""
-    _need(q, torch.float16, "q", 4)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
-    B, q_len, Hq, D = q.shape
-    if query_pos is not None:
-        _need(query_pos, torch.int32, "query_pos", 2)
-        if tuple(query_pos.shape) != (B, q_len):
-            raise ValueError("query_pos must be [batch][q_len]")
     cs = cache.struct()
-    if D != cs.head_dim:
-        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    dev = cache.k_cache.get_device()
+    B, q_len, Hq, shape = _queries(q, cs)
+    cols = _cols("block_table", block_table)
     with _on(q, stream):
         if out is None:
             out = torch.empty_like(q)
-        _need(out, torch.float16, "out", 4)
-        if lse is not None:
-            _need(lse, torch.float32, "lse", 3)
-        _batch(B, q, out, lse, block_table, context_lens)
         if workspace is None and B:   # contents need not be initialised
             need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len)
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws, wbytes = _scratch(workspace, dev)
+        _arg("query_pos", query_pos, torch.int32, (B, q_len), dev)
         opts = _opts(sliding_window, query_pos)
         _check(_lib().pkvq_paged_attn_decode_ex(
-            ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(block_table),
-            int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq, int(max_context_len),
-            float(softmax_scale), None if opts is None else ctypes.byref(opts), _ptr(workspace),
-            wbytes, _stream(stream)), "paged_attn_decode")
+            ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
+            _arg("out", out, torch.float16, shape, dev),
+            _arg("lse", lse, torch.float32, shape[:3], dev),
+            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            int(max_context_len), float(softmax_scale),
+            None if opts is None else ctypes.byref(opts), ws, wbytes, _stream(stream, dev)),
+            "paged_attn_decode")
     return out
 
 
@@ -480,33 +525,29 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
     (zero the entries of new tokens).  Input of kv_evict."""
     cs = cache.struct()
     dev = cache.k_cache.get_device()
-    _need(q, torch.float16, "q", 4)
-    B, q_len, Hq, D = q.shape
-    if D != cs.head_dim:
-        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    B, q_len, Hq, shape = _queries(q, cs)
+    cols = _cols("block_table", block_table)
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+        raise ValueError("weights must be [batch][num_kv_heads][positions]")
+    W = weights.shape[2]
     with _on(q, stream):
         if out is None:
             out = torch.empty_like(q)
-        _args(dev, q=(q, torch.float16, (B, q_len, Hq, D)),
-              out=(out, torch.float16, (B, q_len, Hq, D)), lse=(lse, torch.float32, (B, q_len, Hq)),
-              block_table=(block_table, torch.int32, (B, block_table.shape[-1])),
-              context_lens=(context_lens, torch.int32, (B,)),
-              weights=(weights, torch.float32, (B, cache.num_kv_heads, weights.shape[-1])))
         if workspace is None and B:   # contents need not be initialised
             need = decode_weights_workspace_bytes(cache, B, q_len, Hq, max_context_len)
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        wbytes = 0
-        if workspace is not None:
-            if workspace.get_device() != dev or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be contiguous on cuda:{dev}")
-            wbytes = workspace.numel() * workspace.element_size()
+        ws, wbytes = _scratch(workspace, dev)
         opts = _opts(sliding_window, None)
         _check(_lib().pkvq_paged_attn_decode_weights(
-            ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(block_table),
-            int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq, int(max_context_len),
-            float(softmax_scale), None if opts is None else ctypes.byref(opts), _ptr(weights),
-            int(weights.shape[2]), _ptr(workspace), wbytes, _stream(stream, q.device)),
-            "paged_attn_decode_weights")
+            ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
+            _arg("out", out, torch.float16, shape, dev),
+            _arg("lse", lse, torch.float32, shape[:3], dev),
+            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            int(max_context_len), float(softmax_scale),
+            None if opts is None else ctypes.byref(opts),
+            _arg("weights", weights, torch.float32, (B, cs.num_kv_heads, W), dev), W, ws, wbytes,
+            _stream(stream, dev)), "paged_attn_decode_weights")
     return out
 
 
@@ -523,31 +564,32 @@ def kv_evict(cache: PagedKVCache, weights: torch.Tensor, block_table: torch.Tens
     int32 [B][Hkv][budget]: the kept positions, -1 behind the last)."""
     cs = cache.struct()
     dev = cache.k_cache.get_device()
-    B, H = int(context_lens.shape[0]), cache.num_kv_heads
-    budget = int(budget)
+    B, H, budget = _rows("context_lens", context_lens), cs.num_kv_heads, int(budget)
+    cols, dst_cols = _cols("block_table", block_table), _cols("dst_block_table", dst_block_table)
     if budget < 1:
         raise ValueError("budget must be at least 1")
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+        raise ValueError("weights must be [batch][num_kv_heads][positions]")
+    W = weights.shape[2]
     with _on(weights, stream):
         if weights_out is None:
-            weights_out = torch.empty((B, H, max(weights.shape[-1], budget)), dtype=torch.float32,
+            weights_out = torch.empty((B, H, max(W, budget)), dtype=torch.float32,
                                       device=weights.device)
         if keep is None:
             keep = torch.empty((B, H, budget), dtype=torch.int32, device=weights.device)
         if new_context_lens is None:
             new_context_lens = torch.empty_like(context_lens)
-        _args(dev, weights=(weights, torch.float32, (B, H, weights.shape[-1])),
-              block_table=(block_table, torch.int32, (B, block_table.shape[-1])),
-              context_lens=(context_lens, torch.int32, (B,)),
-              dst_block_table=(dst_block_table, torch.int32, (B, dst_block_table.shape[-1])),
-              weights_out=(weights_out, torch.float32, (B, H, weights_out.shape[-1])),
-              keep=(keep, torch.int32, (B, H, budget)),
-              new_context_lens=(new_context_lens, torch.int32, (B,)))
+        w_out = weights_out.shape[-1]
         _check(_lib().pkvq_kv_evict(
-            ctypes.byref(cs), _ptr(weights), int(weights.shape[2]), _ptr(block_table),
-            int(block_table.shape[1]), _ptr(context_lens), B, budget, int(num_sink),
-            int(num_recent), _ptr(dst_block_table), int(dst_block_table.shape[1]), _ptr(keep),
-            _ptr(new_context_lens), _ptr(weights_out), int(weights_out.shape[2]),
-            _stream(stream, weights.device)), "kv_evict")
+            ctypes.byref(cs), _arg("weights", weights, torch.float32, (B, H, W), dev), W,
+            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, budget,
+            int(num_sink), int(num_recent),
+            _arg("dst_block_table", dst_block_table, torch.int32, (B, dst_cols), dev), dst_cols,
+            _arg("keep", keep, torch.int32, (B, H, budget), dev),
+            _arg("new_context_lens", new_context_lens, torch.int32, (B,), dev),
+            _arg("weights_out", weights_out, torch.float32, (B, H, w_out), dev), w_out,
+            _stream(stream, dev)), "kv_evict")
     return new_context_lens, weights_out, keep
 
 
@@ -562,35 +604,29 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
     are the keys and values of each sequence's last q_len positions; they are
     quantised into the cache (as kv_write_quant) and attention runs as
     paged_attn_decode."""
-    _need(q, torch.float16, "q", 4)
-    _need(k_new, torch.float16, "k_new", 4)
-    _need(v_new, torch.float16, "v_new", 4)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
-    B, q_len, Hq, D = q.shape
-    if tuple(k_new.shape) != (B, q_len, cache.num_kv_heads, D) or k_new.shape != v_new.shape:
-        raise ValueError("k_new / v_new must be [batch][q_len][num_kv_heads][head_dim]")
     cs = cache.struct()
-    if D != cs.head_dim:
-        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    dev = cache.k_cache.get_device()
+    B, q_len, Hq, shape = _queries(q, cs)
+    cols = _cols("block_table", block_table)
+    new = (B, q_len, cs.num_kv_heads, cs.head_dim)
     with _on(q, stream):
         if out is None:
             out = torch.empty_like(q)
-        _need(out, torch.float16, "out", 4)
-        if lse is not None:
-            _need(lse, torch.float32, "lse", 3)
-        _batch(B, q, out, lse, block_table, context_lens)
         if workspace is None and B:   # contents need not be initialised
             need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len)
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws, wbytes = _scratch(workspace, dev)
         opts = _opts(sliding_window, None)
         _check(_lib().pkvq_paged_attn_decode_append(
-            ctypes.byref(cs), _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(out), _ptr(lse),
-            _ptr(block_table), int(block_table.shape[1]), _ptr(context_lens), B, q_len, Hq,
+            ctypes.byref(cs), _arg("k_new", k_new, torch.float16, new, dev),
+            _arg("v_new", v_new, torch.float16, new, dev),
+            _arg("q", q, torch.float16, shape, dev), _arg("out", out, torch.float16, shape, dev),
+            _arg("lse", lse, torch.float32, shape[:3], dev),
+            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
-            None if opts is None else ctypes.byref(opts), _ptr(workspace), wbytes,
-            _stream(stream)), "paged_attn_decode_append")
+            None if opts is None else ctypes.byref(opts), ws, wbytes, _stream(stream, dev)),
+            "paged_attn_decode_append")
     return out
 
 
@@ -600,30 +636,25 @@ def paged_attn_prefill(cache: PagedKVCache, q: torch.Tensor, cu_seqlens_q: torch
                        lse: Optional[torch.Tensor] = None, stream=None,
                        sliding_window: int = 0) -> torch.Tensor:
     """q fp16 [total_q][Hq][D] (packed varlen) -> out fp16 [total_q][Hq][D]."""
-    _need(q, torch.float16, "q", 3)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
-    total_q, Hq, D = q.shape
-    B = int(context_lens.shape[0])
-    if cu_seqlens_q.shape[0] != B + 1:
-        raise ValueError("cu_seqlens_q must have one entry more than context_lens")
     cs = cache.struct()
-    if D != cs.head_dim:
-        raise ValueError(f"q must have head_dim {cs.head_dim}")
+    dev = cache.k_cache.get_device()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != cs.head_dim:
+        raise ValueError(f"q must be [total_q][num_q_heads][{cs.head_dim}]")
+    shape = tuple(q.shape)
+    B, cols = _rows("context_lens", context_lens), _cols("block_table", block_table)
     with _on(q, stream):
         if out is None:
             out = torch.empty_like(q)
-        _need(out, torch.float16, "out", 3)
-        if lse is not None:
-            _need(lse, torch.float32, "lse", 2)
-        _batch(B, q, out, lse, block_table, context_lens)
         opts = _opts(sliding_window, None)
         _check(_lib().pkvq_paged_attn_prefill_ex(
-            ctypes.byref(cs), _ptr(q), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
-            _ptr(block_table), int(block_table.shape[1]), _ptr(context_lens), B, int(max_q_len),
-            Hq, float(softmax_scale), None if opts is None else ctypes.byref(opts), None, 0,
-            _stream(stream)), "paged_attn_prefill")
+            ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
+            _arg("out", out, torch.float16, shape, dev),
+            _arg("lse", lse, torch.float32, shape[:2], dev),
+            _arg("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev),
+            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_q_len),
+            shape[1], float(softmax_scale), None if opts is None else ctypes.byref(opts), None,
+            0, _stream(stream, dev)), "paged_attn_prefill")
     return out
 
 
@@ -671,11 +702,11 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     with _on(q, stream):
         if out is None:
             out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        _args(dev, out=(out, q.dtype, (T, Hq, D)), lse=(lse, torch.float32, (T, Hq)))
         _check(_lib().pkvq_prompt_attn(
-            ctypes.byref(ps), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
-            int(cu_seqlens.shape[0]) - 1, int(max_len), float(softmax_scale),
-            int(sliding_window), _stream(stream, q.device)), "prompt_attn")
+            ctypes.byref(ps), _arg("out", out, q.dtype, (T, Hq, D), dev),
+            _arg("lse", lse, torch.float32, (T, Hq), dev), cu_seqlens.data_ptr(),
+            cu_seqlens.shape[0] - 1, int(max_len), float(softmax_scale), int(sliding_window),
+            _stream(stream, dev)), "prompt_attn")
     return out
 
 
