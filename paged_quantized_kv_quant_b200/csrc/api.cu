@@ -587,8 +587,16 @@ pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights, int64_t
     if (batch == 0)
         return PKVQ_OK;
     if (!weights || !block_table || !context_lens || !dst_block_table || !keep_out ||
-        !new_context_lens || weights_out == weights || new_context_lens == context_lens)
+        !new_context_lens || new_context_lens == context_lens)
         return PKVQ_ERR_INVALID_ARG;
+    if (weights_out) {   // the two accumulators must not overlap
+        const uintptr_t rows = (uintptr_t)batch * (uintptr_t)cache->num_kv_heads;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(weights);
+        const uintptr_t b = reinterpret_cast<uintptr_t>(weights_out);
+        if (a < b + rows * (uintptr_t)weight_out_stride * 4 &&
+            b < a + rows * (uintptr_t)weight_stride * 4)
+            return PKVQ_ERR_INVALID_ARG;
+    }
     EvictParams p{};
     p.k_cache = static_cast<uint8_t *>(cache->k_cache);
     p.v_cache = static_cast<uint8_t *>(cache->v_cache);

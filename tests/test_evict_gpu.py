@@ -128,6 +128,44 @@ def test_evict(fmt, ctx, budget, sink, recent, bs):
     assert pk.device_status() == 0
 
 
+@pytest.mark.parametrize("n,stride,budget,sink,recent", [
+    (40_000, 40_000, 5001, 4, 333),          # a whole cluster, odd slices
+    (40_000, 70_000, 39_999, 0, 0),          # one token goes
+    (20_001, 20_001, 17, 3, 5),
+    (4097, 500_000, 100, 4, 4),              # a row much shorter than its stride
+    (400_000, 400_001, 1000, 4, 64)])        # keys do not fit shared memory
+def test_evict_long_rows(n, stride, budget, sink, recent):
+    bs, hkv = 64, 2
+    r = np.random.default_rng(48)
+    blocks, table, dst = lay_out([n, n // 3], bs, 49, spare=-(-budget // bs))
+    cache = pk.PagedKVCache.allocate(pk.KV_FP8_E4M3, blocks, bs, hkv, k_scale=[1.0] * hkv, v_scale=[1.0] * hkv)
+    g = torch.Generator(device="cuda").manual_seed(50)
+    for t in (cache.k_cache, cache.v_cache):
+        t.random_(0, 127, generator=g)
+    w = np.exp(2 * r.standard_normal((2, hkv, stride))).astype(np.float32)
+    w[:, 1] = np.floor(w[:, 1])              # ties by the thousand
+    ctx = np.int32([n, n // 3])
+    kc, vc = cache.k_cache.clone(), cache.v_cache.clone()
+    lens, wout, keep = pk.kv_evict(cache, cuda(w), cuda(table), cuda(ctx), cuda(dst), budget, sink, recent)
+    keep, wout = keep.cpu().numpy(), wout.cpu().numpy()
+    for b, c in enumerate(ctx):
+        m = min(c, budget)
+        assert int(lens[b]) == m
+        for h in range(hkv):
+            if c <= budget:
+                pick = np.arange(c)
+            else:
+                mid = w[b, h, sink:c - recent]
+                best = np.argsort(-mid, kind="stable")[:budget - sink - recent] + sink
+                pick = np.concatenate([np.arange(sink), np.sort(best), np.arange(c - recent, c)])
+            assert np.array_equal(keep[b, h, :m], pick) and (keep[b, h, m:] == -1).all()
+            assert np.array_equal(wout[b, h, :m], w[b, h, pick]) and (wout[b, h, m:] == 0).all()
+            src, to = table[b][pick // bs], dst[b][np.arange(m) // bs]
+            for new, old in ((cache.k_cache, kc), (cache.v_cache, vc)):
+                assert torch.equal(new[cuda(to).long(), h, cuda(np.arange(m) % bs)],
+                                   old[cuda(src).long(), h, cuda(pick % bs)])
+
+
 def test_evict_odd_weights():
     """Infinities, NaN, negative and signed zero weights have a fixed order."""
     fmt, bs, hkv, n, budget = pk.KV_FP8_E4M3, 16, 1, 64, 24

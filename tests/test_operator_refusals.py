@@ -110,6 +110,8 @@ def test_evict_refusals(lib):
     assert evict(lib, c, dstb=3) == INVALID           # 3 * 16 < 64
     assert evict(lib, c, wos=63) == INVALID
     assert evict(lib, c, wo=0x10000) == INVALID       # in place
+    assert evict(lib, c, wo=0x10000 + 4 * (4 * 500 - 1)) == INVALID   # the last weight
+    assert evict(lib, c, wo=0x10000 - 4 * (4 * 500 - 1)) == INVALID
     assert evict(lib, c, lens=0x30000) == INVALID     # in place
     for name in ("w", "bt", "ctx", "dst", "keep", "lens"):
         assert evict(lib, c, **{name: None}) == INVALID
