@@ -13,12 +13,14 @@
 // of its group and a diagonal tile wastes little.  Tensor memory: S_A, S_B
 // (128 columns each; P over the first 64 of its S), O_A, O_B (128 each).  While
 // one tile's softmax runs, the tensor core runs the other's products.
-// Warp roles (10 warps):
+// Warp roles (12 warps; the third warpgroup gives most of its registers to the
+// softmax, whose 128 scores per thread stay in registers):
 //   warps 0-3  softmax of tile A, warps 4-7 of tile B: thread i owns row i.
 //   warp 8     TMA producer: Q tiles (one 3-D box: 64 d x G heads x tokens, so
 //              the rows land packed), then K(j), V(j) through a ring of 32 KB
 //              stages; any token and head stride that TMA takes serves.
-//   warp 9     issues every MMA: P V then the next S of each tile in turn.
+//   warp 9     issues every MMA: P V then the next S of each tile in turn; P
+//              arrives in two halves, so P V starts during the exponentials.
 // A sequence's last K/V tile may run into the next sequence: scores behind the
 // end are masked, and the V rows there are zeroed in shared memory first (0
 // times another prompt's infinity would be NaN).
@@ -33,7 +35,7 @@
 namespace pkvq {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kKT = 128;          // keys per tile
 constexpr int kStages = 5;        // ring of K and V tiles
 constexpr int kTile = 32768;      // 128 rows x 128 x 2 bytes, two 64-wide halves
@@ -48,7 +50,7 @@ constexpr uint32_t kTmS = 0, kTmO = 256;   // + 128 * tile
 constexpr int kOffQ = 0;                          // 2 tiles
 constexpr int kOffKV = 2 * kTile;                 // kStages tiles
 constexpr int kOffBars = kOffKV + kStages * kTile;
-constexpr int kNumBars = 2 + 2 * kStages + 3 * 2 + 1;
+constexpr int kNumBars = 2 + 2 * kStages + 4 * 2 + 1;
 constexpr int kOffTaddr = kOffBars + kNumBars * 8;
 constexpr size_t kSmemAlloc = kOffTaddr + 16 + 1024;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
@@ -56,7 +58,8 @@ static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 struct Bars {
     uint64_t *q_full;                  // [tile]
     uint64_t *kv_full, *kv_empty;      // [kStages]
-    uint64_t *s_full, *p_full, *pv_done;   // [tile]
+    uint64_t *s_full, *pv_done;        // [tile]
+    uint64_t *p_full;                  // [tile][half]
     uint64_t *mma_done;
 };
 
@@ -69,7 +72,7 @@ __device__ __forceinline__ Bars carve_bars(uint8_t *smem)
     r.kv_empty = r.kv_full + kStages;
     r.s_full = r.kv_empty + kStages;
     r.p_full = r.s_full + 2;
-    r.pv_done = r.p_full + 2;
+    r.pv_done = r.p_full + 4;
     r.mma_done = r.pv_done + 2;
     return r;
 }
@@ -101,6 +104,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     } else {
         return pack_half2(lo, hi);
     }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Geometry of one query tile: key tiles jbase .. jbase + ntiles - 1.
@@ -152,7 +162,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.q_full[i], 1);
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.p_full[2 * i], 4);
+            mbar_init(&bars.p_full[2 * i + 1], 4);
             mbar_init(&bars.pv_done[i], 1);
         }
         for (int s = 0; s < kStages; ++s) {
@@ -171,6 +182,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     tc_fence_after();
     const uint32_t tmem = *taddr_smem;
 
+    // 384 x 168 registers at launch: 128 x 80 + 256 x 208 fit in them
+    if (warp >= kWarpLoad) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kWarpLoad) {
         // ---------------------------------------------- copy producer --
         // ring entry i: K(i / 2) for even i, V(i / 2) for odd i
@@ -252,15 +266,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                 __syncwarp();
                 v_clean = true;
             }
-            if (!warp_wait(&bars.p_full[x], j & 1, p.status))
-                return false;
-            tc_fence_after();
             const uint64_t vd = vd0 + (uint64_t)((s * kTile) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kKT / 16; ++ks)
-                mma_f16_ts_elect(tmem + kTmO + x * 128, tmem + kTmS + x * 128 + ks * 8,
-                                 vd + (uint64_t)((ks * 2048) >> 4), kIdescPV,
-                                 (j > 0 || ks > 0) ? 1u : 0u);
+            for (int half = 0; half < 2; ++half) {
+                if (!warp_wait(&bars.p_full[2 * x + half], j & 1, p.status))
+                    return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                    mma_f16_ts_elect(tmem + kTmO + x * 128, tmem + kTmS + x * 128 + ks * 8,
+                                     vd + (uint64_t)((ks * 2048) >> 4), kIdescPV,
+                                     (j > 0 || ks > 0) ? 1u : 0u);
+            }
             if (j == qt[x].ntiles - 1)
                 mma_commit_elect(&bars.pv_done[x]);
             if (x == 1 || j >= qt[1].ntiles)
@@ -279,7 +296,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                     ok = pv(x, j) && (j + 1 >= qt[x].ntiles || qk(x, j + 1));
         mma_commit_elect(bars.mma_done);
         warp_wait(bars.mma_done, 0, p.status);
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ------------------------------------------------------ softmax --
         const int x = warp >> 2;
         const int r = tid - 128 * x;         // row == TMEM lane
@@ -323,16 +342,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                     if (key0 + c > pos || key0 + c < lo)
                         v[c] = -INFINITY;
             }
-            float m8[8];
+            float m8[8];   // eight independent chains of three-input maxima
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                m8[i] = v[i];
+                m8[i] = fmaxf(v[i], v[i + 8]);
 #pragma unroll
-                for (int c = i + 8; c < kKT; c += 8)
-                    m8[i] = fmaxf(m8[i], v[c]);
+                for (int c = i + 16; c < kKT; c += 16)
+                    m8[i] = max3(m8[i], v[c], v[c + 8]);
             }
-            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
+                                  fmaxf(m8[6], m8[7]));
             // lazy rescale: only when the max grew by more than 2^8
             const bool need = m_used != -INFINITY && (mx - m_used) * kf > kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
@@ -369,14 +388,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                     pk[c / 2] = pack2<BF>(e.x, e.y);
                 }
                 tmem_st16(ts + 16 * g, pk);
+                if (g & 1) {   // 64 keys of P
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.p_full[2 * x + (g >> 1)]);
+                }
             }
             const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
             l += a.x + a.y;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.p_full[x]);
         }
 
         // ---- epilogue: O / l ----
