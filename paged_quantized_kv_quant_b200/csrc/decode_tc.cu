@@ -47,10 +47,10 @@
 // an FP32 partial (unnormalised O, max in log2 units, sum) in the decode
 // workspace, which the decode merge kernel combines.
 //
-// Block-scaled formats (a K and a V scale per block and KV head): the K warps
-// hand the softmax each key's score factor, the V warps log2 of its V scale;
-// the softmax takes p' = 2^(s + log2 vs - M), l += p' / vs, and the codes enter
-// the tensor core exactly.
+// Block-scaled formats (a K and a V scale per block and KV head): the dequant
+// warps hand the softmax three factors for each 16 keys (K warps the first, V
+// warps the others); it takes p' = 2^(s + log2 vs - M), l += p' / vs, and the codes
+// enter the tensor core exactly.
 //
 // FP16 caches need no conversion: warp 9 copies each key's two 128-byte row
 // halves straight into a K/V buffer (the same swizzled layout) with cp.async,
@@ -106,10 +106,9 @@ constexpr int kOffCodes = kOffKV + kKVBufs * kKVBuf;
 constexpr int kCodeStage = 16384;
 constexpr int kOffScl = kOffCodes + kCodeStages * kCodeStage;   // stages x 8 warps x 32 halves (16 used)
 constexpr int kOffKsf = kOffScl + kCodeStages * kDequantWarps * 64;   // bufs x 64 fp32 K factors
-// block-scaled formats: bufs x 64 fp32 log2 V scales, bufs x 4 fp32 1 / V scale (16 keys each)
-constexpr int kOffLvf = kOffKsf + kKVBufs * 64 * 4;
-constexpr int kOffIvf = kOffLvf + kKVBufs * 64 * 4;
-constexpr int kOffBars = kOffIvf + kKVBufs * 4 * 4;
+// (block-scaled formats: per buffer, 4 x ks, 4 x lv, 4 x iv of its four 16-key
+// groups, see BlockFactors, at the start of its 64)
+constexpr int kOffBars = kOffKsf + kKVBufs * 64 * 4;
 constexpr int kNumBars = 1 + 3 * kKVBufs + 3 * kSBufs + 2;
 constexpr int kOffTaddr = kOffBars + kNumBars * 8;
 constexpr int kOffProgress = kOffTaddr + 8;   // tiles dequantised so far (prefetch pacing)
@@ -493,16 +492,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if constexpr (kv_has_block_scale(KVT)) {
                     const float sb = *reinterpret_cast<const float *>(
                         smem + kOffScl + (st * kDequantWarps + warp) * 64);
-                    if (!isv && dh == 0)
-                        reinterpret_cast<float *>(smem + kOffKsf)[bj * 64 + row] =
-                            live ? kfac * sb : 0.0f;
-                    if (isv && dh == 0) {
-                        // scale 0: every code of the block is 0, any factor serves
-                        const float vs = live && sb > 0.0f ? sb : 1.0f;
-                        reinterpret_cast<float *>(smem + kOffLvf)[bj * 64 + row] = log2f(vs);
-                        if (lane == 0)
-                            reinterpret_cast<float *>(smem + kOffIvf)[bj * 4 + (warp & 3)] =
-                                __frcp_rn(vs);
+                    if (lane == 0) {   // (this lane's row is the group's first)
+                        const BlockFactors f(kfac, sb, sb, live);
+                        float *dst =
+                            reinterpret_cast<float *>(smem + kOffKsf) + bj * 64 + (warp & 3);
+                        if (isv)
+                            dst[4] = f.lv, dst[8] = f.iv;
+                        else
+                            dst[0] = f.ks;
                     }
                 }
                 fence_async_smem();
@@ -603,17 +600,18 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             }
             const int tile0 = key_begin + j * kKT;   // first key of the tile
             const int key0 = tile0 + kh * kCols;     // first key of this thread's scores
+            constexpr int kGroups = kCols / 16;
+            float bks[kGroups], blv[kGroups], biv[kGroups];
             if constexpr (kv_has_block_scale(KVT)) {
-                const float *ksf =
-                    reinterpret_cast<const float *>(smem + kOffKsf) + (j % kKVBufs) * 64 + kh * kCols;
-                const float *lvf =
-                    reinterpret_cast<const float *>(smem + kOffLvf) + (j % kKVBufs) * 64 + kh * kCols;
+                const float *f = reinterpret_cast<const float *>(smem + kOffKsf) +
+                                 (j % kKVBufs) * 64 + kh * kGroups;
 #pragma unroll
-                for (int c = 0; c < kCols; c += 2) {
-                    const float2 r2 = __ffma2_rn(make_float2(v[c], v[c + 1]),
-                                                 make_float2(ksf[c], ksf[c + 1]),
-                                                 make_float2(lvf[c], lvf[c + 1]));
-                    v[c] = r2.x, v[c + 1] = r2.y;
+                for (int i = 0; i < kGroups; ++i)
+                    bks[i] = f[i], blv[i] = f[4 + i], biv[i] = f[8 + i];
+                if (kfac < 0.0f) {   // (the group maxima below need positive factors)
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+                        v[c] = -v[c];
                 }
             } else if constexpr (KVT != kKvInt8) {
                 const float2 f2 = make_float2(kfac, kfac);
@@ -642,16 +640,24 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     if (key0 + c > pos || key0 + c >= key_lim || key0 + c < lo)
                         v[c] = -INFINITY;
             }
-            float m8[8];
+            float mx;
+            if constexpr (kv_has_block_scale(KVT)) {
+                mx = fmaf(max16(v), bks[0], blv[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m8[i] = v[i];
+                for (int i = 1; i < kGroups; ++i)
+                    mx = fmaxf(mx, fmaf(max16(v + 16 * i), bks[i], blv[i]));
+            } else {
+                float m8[8];
 #pragma unroll
-                for (int c = i + 8; c < kCols; c += 8)
-                    m8[i] = fmaxf(m8[i], v[c]);
+                for (int i = 0; i < 8; ++i) {
+                    m8[i] = v[i];
+#pragma unroll
+                    for (int c = i + 8; c < kCols; c += 8)
+                        m8[i] = fmaxf(m8[i], v[c]);
+                }
+                mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
             }
-            float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                             fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
             if constexpr (kHalf)   // the row's other key half
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             // lazy rescale: only when the max grew by more than 2^8
@@ -692,7 +698,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                     const int cc = 32 * g + c;
-                    const float2 d = __fadd2_rn(make_float2(v[cc], v[cc + 1]), nmu);
+                    float2 d;
+                    if constexpr (kv_has_block_scale(KVT)) {
+                        const float k_ = bks[cc >> 4], o_ = blv[cc >> 4] - mu;
+                        d = __ffma2_rn(make_float2(v[cc], v[cc + 1]), make_float2(k_, k_),
+                                       make_float2(o_, o_));
+                    } else {
+                        d = __fadd2_rn(make_float2(v[cc], v[cc + 1]), nmu);
+                    }
                     const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                     // (block-scaled: one sum for each 16 keys, which share a V scale)
                     const int ai = kv_has_block_scale(KVT) ? cc >> 4 : (c >> 1) & 3;
@@ -705,11 +718,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     tmem_st16(tl + kTmS + sbuf(j) * kKT + 16 * g, pk);
             }
             if constexpr (kv_has_block_scale(KVT)) {
-                const float *ivf = reinterpret_cast<const float *>(smem + kOffIvf) +
-                                   (j % kKVBufs) * 4 + kh * (kCols / 16);
 #pragma unroll
-                for (int i = 0; i < kCols / 16; ++i)
-                    l = fmaf(acc[i].x + acc[i].y, ivf[i], l);
+                for (int i = 0; i < kGroups; ++i)
+                    l = fmaf(acc[i].x + acc[i].y, biv[i], l);
             } else {
                 const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
                 const float2 a = __fadd2_rn(a01, a23);

@@ -36,9 +36,10 @@
 //               softmax runs.
 //
 // Block-scaled formats (a K and a V scale per block and KV head): the dequant
-// warps hand the softmax each key's score factor (K scale) and log2 of its V
-// scale, and the softmax takes p' = 2^(s + log2 vs - M), l += p' / vs: codes
-// enter the tensor core exactly and no V element is multiplied.
+// warps hand the softmax three factors for each 16 keys, and the softmax takes
+// p' = 2^(s + log2 vs - M), l += p' / vs: codes enter the tensor core exactly, no
+// V element is multiplied, and scaling the scores costs nothing (the maximum is
+// taken per group of 16 before it, and it shares the exponent's multiply-add).
 //
 // FP16 caches need no conversion: the TMA warp copies each block's two
 // 128-byte row halves straight into a K/V buffer, and the dequant warps only
@@ -81,10 +82,9 @@ constexpr int kOffCodes = kOffKV + kKVBufs * kKVBuf;      // stages x (K 8K, V 8
 constexpr int kCodeStage = 16384;
 constexpr int kOffScl = kOffCodes + kCodeStages * kCodeStage;   // stages x (K 64, V 64) halves
 constexpr int kOffKsf = kOffScl + kCodeStages * 256;            // bufs x 64 fp32 K factors
-// block-scaled formats: bufs x 64 fp32 log2 V scales, bufs x 4 fp32 1 / V scale (16 keys each)
-constexpr int kOffLvf = kOffKsf + kKVBufs * 64 * 4;
-constexpr int kOffIvf = kOffLvf + kKVBufs * 64 * 4;
-constexpr int kOffBars = kOffIvf + kKVBufs * 4 * 4;
+// (block-scaled formats: per buffer, 4 x ks, 4 x lv, 4 x iv of its four 16-key
+// groups, see BlockFactors, at the start of its 64)
+constexpr int kOffBars = kOffKsf + kKVBufs * 64 * 4;
 constexpr int kNumBars = 1 + 2 * kCodeStages + 3 * kKVBufs + 3 * 2 + 1;
 constexpr int kOffTaddr = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffTaddr + 16;
@@ -457,14 +457,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     key0 + row < ctx ? kfac * __half2float(__ushort_as_half(scl[row])) : 0.0f;
             }
             if constexpr (kv_has_block_scale(KVT)) {
-                // scale 0: every code of the block is 0, any factor serves
-                const float *sb = reinterpret_cast<const float *>(scl) + row / BS;
-                const bool live = key0 + row < ctx;
-                const float vs = live && sb[4] > 0.0f ? sb[4] : 1.0f;
-                reinterpret_cast<float *>(smem + kOffKsf)[bj * 64 + row] = live ? kfac * sb[0] : 0.0f;
-                reinterpret_cast<float *>(smem + kOffLvf)[bj * 64 + row] = log2f(vs);
-                if ((row & 15) == 0)
-                    reinterpret_cast<float *>(smem + kOffIvf)[bj * 4 + row / 16] = __frcp_rn(vs);
+                if ((row & 15) == 0) {
+                    const float *sb = reinterpret_cast<const float *>(scl) + row / BS;
+                    const BlockFactors f(kfac, sb[0], sb[4], key0 + row < ctx);
+                    float *dst = reinterpret_cast<float *>(smem + kOffKsf) + bj * 64 + row / 16;
+                    dst[0] = f.ks, dst[4] = f.lv, dst[8] = f.iv;
+                }
             }
             fence_async_smem();
             __syncwarp();
@@ -539,17 +537,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             }
 
             const int key0 = (jbase + j) * kKT;
+            float bks[4], blv[4], biv[4];
             if constexpr (kv_has_block_scale(KVT)) {
-                const float *ksf =
-                    reinterpret_cast<const float *>(smem + kOffKsf) + (j % kKVBufs) * 64;
-                const float *lvf =
-                    reinterpret_cast<const float *>(smem + kOffLvf) + (j % kKVBufs) * 64;
+                const float4 *f = reinterpret_cast<const float4 *>(smem + kOffKsf) + (j % kKVBufs) * 16;
+                const float4 a = f[0], b4 = f[1], c4 = f[2];
+                bks[0] = a.x, bks[1] = a.y, bks[2] = a.z, bks[3] = a.w;
+                blv[0] = b4.x, blv[1] = b4.y, blv[2] = b4.z, blv[3] = b4.w;
+                biv[0] = c4.x, biv[1] = c4.y, biv[2] = c4.z, biv[3] = c4.w;
+                if (kfac < 0.0f) {   // (the group maxima below need positive factors)
 #pragma unroll
-                for (int c = 0; c < kKT; c += 2) {
-                    const float2 r2 = __ffma2_rn(make_float2(v[c], v[c + 1]),
-                                                 make_float2(ksf[c], ksf[c + 1]),
-                                                 make_float2(lvf[c], lvf[c + 1]));
-                    v[c] = r2.x, v[c + 1] = r2.y;
+                    for (int c = 0; c < kKT; ++c)
+                        v[c] = -v[c];
                 }
             } else if constexpr (KVT != kKvInt8) {
                 const float2 f2 = make_float2(kfac, kfac);
@@ -575,17 +573,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     if (key0 + c > pos || key0 + c < lo)
                         v[c] = -INFINITY;
             }
-            // row max: eight independent chains, then a tree
-            float m8[8];
+            float mx;
+            if constexpr (kv_has_block_scale(KVT)) {
+                mx = fmaxf(max3(fmaf(max16(v), bks[0], blv[0]), fmaf(max16(v + 16), bks[1], blv[1]),
+                                fmaf(max16(v + 32), bks[2], blv[2])),
+                           fmaf(max16(v + 48), bks[3], blv[3]));
+            } else {
+                // row max: eight independent chains, then a tree
+                float m8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m8[i] = v[i];
+                for (int i = 0; i < 8; ++i) {
+                    m8[i] = v[i];
 #pragma unroll
-                for (int c = i + 8; c < kKT; c += 8)
-                    m8[i] = fmaxf(m8[i], v[c]);
+                    for (int c = i + 8; c < kKT; c += 8)
+                        m8[i] = fmaxf(m8[i], v[c]);
+                }
+                mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
             }
-            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
             // lazy rescale: only when the max grew by more than 2^8
             const bool need = m_used != -INFINITY && mx > m_used + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
@@ -613,7 +618,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             uint32_t pk[kKT / 2];
 #pragma unroll
             for (int c = 0; c < kKT; c += 2) {
-                const float2 d = __fadd2_rn(make_float2(v[c], v[c + 1]), nmu);
+                float2 d;
+                if constexpr (kv_has_block_scale(KVT)) {
+                    const float k_ = bks[c >> 4], o_ = blv[c >> 4] - mu;
+                    d = __ffma2_rn(make_float2(v[c], v[c + 1]), make_float2(k_, k_),
+                                   make_float2(o_, o_));
+                } else {
+                    d = __fadd2_rn(make_float2(v[c], v[c + 1]), nmu);
+                }
                 const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                 // (block-scaled: one sum for each 16 keys, which share a V scale)
                 const int ai = kv_has_block_scale(KVT) ? c >> 4 : (c >> 1) & 3;
@@ -621,10 +633,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 pk[c / 2] = pack_half2(e.x, e.y);
             }
             if constexpr (kv_has_block_scale(KVT)) {
-                const float *ivf = reinterpret_cast<const float *>(smem + kOffIvf) + (j % kKVBufs) * 4;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    l = fmaf(acc[i].x + acc[i].y, ivf[i], l);
+                    l = fmaf(acc[i].x + acc[i].y, biv[i], l);
             } else {
                 const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
                 const float2 a = __fadd2_rn(a01, a23);

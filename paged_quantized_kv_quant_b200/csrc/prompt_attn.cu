@@ -106,13 +106,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     }
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // Geometry of one query tile: key tiles jbase .. jbase + ntiles - 1.
 struct QTile {
     int q0, pos_hi, ntiles;

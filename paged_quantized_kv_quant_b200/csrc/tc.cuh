@@ -117,6 +117,39 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t *bar)
         : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Largest of 16 values.
+__device__ __forceinline__ float max16(const float *v)
+{
+    const float a = max3(max3(v[0], v[1], v[2]), v[3], v[4]);
+    const float b = max3(max3(v[5], v[6], v[7]), v[8], v[9]);
+    const float c = max3(max3(v[10], v[11], v[12]), v[13], v[14]);
+    return fmaxf(max3(a, b, c), v[15]);
+}
+
+// Factors of a group of 16 keys of one cache block in the block-scaled formats,
+// as the softmax of the tensor-core kernels takes them: a key's exponent is
+// ks * (q . codes) + lv - M and its weight's sum counts iv times, with ks =
+// |softmax scale| log2(e) times the K scale, lv = log2 and iv = 1 / of the V
+// scale.  ks stays positive, so that a masked score, -inf, remains one: where a
+// scale is 0, or the group holds no key, all its codes are 0.
+struct BlockFactors {
+    float ks, lv, iv;
+    __device__ __forceinline__ BlockFactors(float kfac, float k_scale, float v_scale, bool live)
+    {
+        ks = live ? fmaxf(fabsf(kfac) * k_scale, 1e-30f) : 1e-30f;
+        const float vs = live && v_scale > 0.0f ? v_scale : 1.0f;
+        lv = log2f(vs);
+        iv = __frcp_rn(vs);
+    }
+};
+
 #define PKVQ_R32(X)                                                                           \
     "=r"(X[0]), "=r"(X[1]), "=r"(X[2]), "=r"(X[3]), "=r"(X[4]), "=r"(X[5]), "=r"(X[6]),      \
         "=r"(X[7]), "=r"(X[8]), "=r"(X[9]), "=r"(X[10]), "=r"(X[11]), "=r"(X[12]),           \

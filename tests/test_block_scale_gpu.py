@@ -112,7 +112,8 @@ def test_write_skips_positions_below_zero_and_foreign_rows():
     assert_same(cache, host)
 
 
-def check_rows(out, lse, q, host, table, b, ctx, pos, hq, window=0, what=""):
+def check_rows(out, lse, q, host, table, b, ctx, pos, hq, window=0, what="",
+               scale=SCALE):
     """out / lse [rows][Hq] of one sequence against the reference."""
     G = hq // host.hkv
     for h in range(host.hkv):
@@ -122,7 +123,7 @@ def check_rows(out, lse, q, host, table, b, ctx, pos, hq, window=0, what=""):
             nb = -(-ctx // host.bs)
             vmax = max(vmax, QMAX[host.fmt] * float(host.vs[table[b][:nb], h].max(initial=0.0)))
         for g in range(h * G, (h + 1) * G):
-            ref, rl, _, a, sabs = attention(q[:, g], keys, vals, pos, SCALE, window)
+            ref, rl, _, a, sabs = attention(q[:, g], keys, vals, pos, scale, window)
             err = np.abs(out[:, g] - ref)
             bound = out_bound(ref, a, ctx, vmax, sabs)
             assert np.isfinite(out[:, g]).all() and (err <= bound).all(), \
@@ -229,6 +230,28 @@ def test_prefill(fmt, hq, hkv, bs, ctx, chunk, window):
         s = slice(cu[b], cu[b + 1])
         check_rows(out[s], lse[s], q[s].astype(float), host, table, b, c, c - n + np.arange(n), hq, window)
     assert pk.device_status() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1e-25])
+@pytest.mark.parametrize("ql,hq", [(1, 8), (5, 16), (12, 16), (150, 8)])
+def test_other_softmax_scales(scale, ql, hq):
+    """Uniform weights and negated scores, in all four kernels (mma.sync decode,
+    tensor-core decode up to 64 and up to 128 rows, prefill)."""
+    fmt, bs, hkv, ctx = pk.KV_INT8_BLOCK, 16, 2, [333]
+    blocks, table, _ = lay_out(ctx, bs, 51)
+    cache = random_cache(fmt, blocks, bs, hkv, 52)
+    host = Host(cache)
+    q = queries(np.random.default_rng(53), ql, hq, D)
+    t, c = cuda(table), cuda(np.int32(ctx))
+    lse = torch.empty((ql, hq), device="cuda")
+    if ql <= 16:
+        out = pk.paged_attn_decode(cache, cuda(q[None]), t, c, 333, scale, lse=lse[None])[0]
+    else:
+        out = pk.paged_attn_prefill(cache, cuda(q), cuda(np.int32([0, ql])), t, c, ql, scale, lse=lse)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    sign = -1.0 if scale < 0 else 1.0     # the reference's magnitudes take |scale|
+    check_rows(out, lse, sign * q.astype(float), host, table, 0, 333, 333 - ql + np.arange(ql), hq,
+               scale=abs(scale))
 
 
 @pytest.mark.parametrize("fmt", BLOCK)
