@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeParams p)
     const int b = (int)(gw / ((long long)p.rows * p.num_kv_heads));
     // slots first .. first + nsplit - 1 of unit (row group, KV head) y
     const int y = (rr / p.rows_per_cta) * p.num_kv_heads + h;
-    MergeRow mr;
+    MergeRow<16> mr;
     mr.row0 = (size_t)y * p.num_splits * p.rows_per_cta + rr % p.rows_per_cta;
     mr.stride = p.rows_per_cta;
     // The slots of sequence b come from the context lengths, inputs the split

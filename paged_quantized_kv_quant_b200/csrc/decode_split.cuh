@@ -363,13 +363,12 @@ __device__ __forceinline__ void append_tokens(const DecodeParams &p, int b, int 
 
 // Merge of the split partial states of one output row by one warp:
 // M = max_i m_i, L = sum_i l_i 2^(m_i - M), O = sum_i O_i 2^(m_i - M) / L.
-// The splits are taken kMergeChunk at a time: every lane issues the loads of
+// The splits are taken kMergeChunk (16 in the merge kernel) at a time: every lane issues the loads of
 // a whole chunk (the (m, l) pairs, the same for all lanes, and its float4 of
 // each O row) before using any, so a chunk costs one memory round trip; the
 // chunks are combined online.  `preloaded`: the caller already loaded the
 // first chunk for slots first .. (ml, v).
-constexpr int kMergeChunk = 16;
-
+template <int kMergeChunk>
 struct MergeRow {
     size_t row0, stride;   // workspace row of the first slot, rows between slots
     float2 ml[kMergeChunk];

@@ -18,7 +18,7 @@ namespace pkvq {
 namespace {
 
 constexpr int kWThreads = 256;
-constexpr int kKeysPerThread = 2;
+constexpr int kKeysPerThread = 4;
 constexpr int kChunk = kWThreads * kKeysPerThread;
 constexpr int kMaxRows = 256;   // 16 query tokens x 16 heads per KV head
 
@@ -26,7 +26,7 @@ constexpr int kMaxRows = 256;   // 16 query tokens x 16 heads per KV head
 // remaining CTAs merge the partial states of 8 output rows each.
 // RR: score rows per key (1, 2, 4, 8), or 0 for any multiple of 4.
 template <int BS, int RR>
-__global__ void __launch_bounds__(kWThreads)
+__global__ void __launch_bounds__(kWThreads, 3)
 decode_weights_kernel(const DecodeParams p, const int chunks)
 {
     __shared__ float lse2[kMaxRows];
@@ -41,7 +41,8 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
     if ((int)blockIdx.x >= chunks) {
         const int rr = ((int)blockIdx.x - chunks) * (kWThreads / 32) + warp;
         if (rr < p.rows && si.nsplit > 1) {   // (a single split wrote the final row itself)
-            MergeRow mr;
+            // (4 splits at a time: the other CTAs pay for this branch's registers)
+            MergeRow<4> mr;
             mr.row0 = (size_t)((rr / p.rows_per_cta) * p.num_kv_heads + h) * p.num_splits *
                           p.rows_per_cta + rr % p.rows_per_cta;
             mr.stride = p.rows_per_cta;
