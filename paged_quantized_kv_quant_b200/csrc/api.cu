@@ -664,7 +664,7 @@ pkvq_status pkvq_prompt_attn(const pkvq_prompt *t, void *out, float *lse_out,
     for (int i = 0; i < 3; ++i)
         if (!make_rows_tensor_map(&m[i], base[i], bf16, t->total,
                                   i == 0 ? t->num_q_heads : t->num_kv_heads, ts[i], hs[i],
-                                  i == 0 ? group : 1, i == 0 ? p.tokens_per_tile : 128))
+                                  i == 0 ? group : 1, i == 0 ? p.tokens_per_tile : kPromptKeys))
             return PKVQ_ERR_CUDA;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse_out;

@@ -194,6 +194,8 @@ struct CopyParams {
 
 cudaError_t launch_copy_blocks(const CopyParams &p, cudaStream_t stream);
 
+constexpr int kPromptKeys = 80;      // keys per tile of the prompt attention kernel
+
 struct PromptParams {
     uint16_t *out;                   // fp16 or bf16 [total][Hq][128]
     float *lse;

@@ -10,17 +10,22 @@
 //
 // A CTA owns two adjacent query tiles A and B of 128 rows: a tile is 128 / G
 // tokens x the G query heads of one KV head, so every K/V tile serves all heads
-// of its group and a diagonal tile wastes little.  Tensor memory: S_A, S_B
-// (128 columns each; P over the first 64 of its S), O_A, O_B (128 each).  While
-// one tile's softmax runs, the tensor core runs the other's products.
-// Warp roles (12 warps; the third warpgroup gives most of its registers to the
-// softmax, whose 128 scores per thread stay in registers):
-//   warps 0-3  softmax of tile A, warps 4-7 of tile B: thread i owns row i.
+// of its group and a diagonal tile wastes little.  Key tiles hold 80 keys: then
+// tensor memory takes, per query tile, S (80 columns), P (40, two per column)
+// and O (128), all apart: S(j+1) = Q K(j+1)^T is issued as soon as the softmax
+// has S(j) in registers, and a tile's softmax never waits for the tensor core.
+// (128-key tiles fit only with P over S; each tile's next S then waited for its
+// P V, 1,600 of 3,800 cycles per tile.)
+// Warp roles (11 warps):
+//   warps 0-3  softmax of tile A, warps 4-7 of tile B: thread i owns row i, its
+//              80 scores in registers.
 //   warp 8     TMA producer: Q tiles (one 3-D box: 64 d x G heads x tokens, so
-//              the rows land packed), then K(j), V(j) through a ring of 32 KB
+//              the rows land packed), then K and V tiles through a ring of 20 KB
 //              stages; any token and head stride that TMA takes serves.
-//   warp 9     issues every MMA: P V then the next S of each tile in turn; P
-//              arrives in two halves, so P V starts during the exponentials.
+//   warp 9     issues S = Q K^T, warp 10 P V, of each tile in turn.  (One issuer
+//              for both spent 100 cycles on each barrier that was already
+//              complete, and an MMA's issue waits for the tensor core to take
+//              it: 2,450 cycles per pair of tiles, half of them issuing.)
 // A sequence's last K/V tile may run into the next sequence: scores behind the
 // end are masked, and the V rows there are zeroed in shared memory first (0
 // times another prompt's infinity would be NaN).
@@ -35,22 +40,25 @@
 namespace pkvq {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kKT = 128;          // keys per tile
-constexpr int kStages = 5;        // ring of K and V tiles
-constexpr int kTile = 32768;      // 128 rows x 128 x 2 bytes, two 64-wide halves
-constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr int kThreads = 352;
+constexpr int kKT = kPromptKeys;  // keys per tile
+constexpr int kStages = 8;        // ring of K and V tiles
+constexpr int kQTile = 32768;     // 128 rows x 128 x 2 bytes, two 64-wide halves
+constexpr int kTile = kKT * 256;
+constexpr int kWarpLoad = 8, kWarpQk = 9, kWarpPv = 10;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.0f;
 
 // tensor memory columns
-constexpr uint32_t kTmS = 0, kTmO = 256;   // + 128 * tile
+constexpr uint32_t kTmS = 0, kTmP = kKT, kTmO = 256;   // + 128 * tile
+static_assert(kKT + kKT / 2 <= 128 && kKT % 16 == 0, "S and P of a tile");
 
 // shared memory, from a 1024-byte aligned base
 constexpr int kOffQ = 0;                          // 2 tiles
-constexpr int kOffKV = 2 * kTile;                 // kStages tiles
+constexpr int kOffKV = 2 * kQTile;                // kStages tiles
 constexpr int kOffBars = kOffKV + kStages * kTile;
-constexpr int kNumBars = 2 + 2 * kStages + 4 * 2 + 1;
+constexpr int kNumBars = 2 + 2 * kStages + 4 * 2 + 2;
+static_assert(kTile % 1024 == 0, "128-byte swizzle");
 constexpr int kOffTaddr = kOffBars + kNumBars * 8;
 constexpr size_t kSmemAlloc = kOffTaddr + 16 + 1024;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
@@ -58,9 +66,9 @@ static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 struct Bars {
     uint64_t *q_full;                  // [tile]
     uint64_t *kv_full, *kv_empty;      // [kStages]
-    uint64_t *s_full, *pv_done;        // [tile]
-    uint64_t *p_full;                  // [tile][half]
-    uint64_t *mma_done;
+    uint64_t *s_full, *s_empty;        // [tile] S written / in registers
+    uint64_t *p_full, *pv_done;        // [tile]
+    uint64_t *mma_done;                // [issuer] its products have retired
 };
 
 __device__ __forceinline__ Bars carve_bars(uint8_t *smem)
@@ -71,8 +79,9 @@ __device__ __forceinline__ Bars carve_bars(uint8_t *smem)
     r.kv_full = r.q_full + 2;
     r.kv_empty = r.kv_full + kStages;
     r.s_full = r.kv_empty + kStages;
-    r.p_full = r.s_full + 2;
-    r.pv_done = r.p_full + 4;
+    r.s_empty = r.s_full + 2;
+    r.p_full = r.s_empty + 2;
+    r.pv_done = r.p_full + 2;
     r.mma_done = r.pv_done + 2;
     return r;
 }
@@ -155,18 +164,19 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.q_full[i], 1);
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[2 * i], 4);
-            mbar_init(&bars.p_full[2 * i + 1], 4);
+            mbar_init(&bars.s_empty[i], 4);
+            mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.pv_done[i], 1);
         }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.kv_full[s], 1);
             mbar_init(&bars.kv_empty[s], 1);
         }
-        mbar_init(bars.mma_done, 1);
+        mbar_init(&bars.mma_done[0], 1);
+        mbar_init(&bars.mma_done[1], 1);
         fence_mbar_init();
     }
-    if (warp == kWarpMma) {
+    if (warp == kWarpQk) {
         tmem_alloc(taddr_smem, 512);
         tmem_relinquish();
         tc_fence_before();
@@ -175,19 +185,19 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     tc_fence_after();
     const uint32_t tmem = *taddr_smem;
 
-    // 384 x 168 registers at launch: 128 x 80 + 256 x 208 fit in them
-    if (warp >= kWarpLoad) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ring entries in the order the MMAs take them: K(0) K(1) V(0) K(2) V(1) ...
+    auto k_entry = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
+    auto v_entry = [&](int j) { return j == ntiles - 1 ? 2 * j + 1 : 2 * j + 2; };
+
     if (warp == kWarpLoad) {
         // ---------------------------------------------- copy producer --
-        // ring entry i: K(i / 2) for even i, V(i / 2) for odd i
         const uint32_t qbytes = (uint32_t)(tpt * G) * 256u;
         auto load_q = [&](int x) {
             if (qt[x].ntiles > 0 && lane == 0) {
                 mbar_arrive_expect_tx(&bars.q_full[x], qbytes);
-                const uint32_t dst = sbase + kOffQ + x * kTile;
+                const uint32_t dst = sbase + kOffQ + x * kQTile;
                 tma_tile_3d_g2s(dst, &qmap, 0, h * G, tok0 + qt[x].q0, &bars.q_full[x]);
-                tma_tile_3d_g2s(dst + kTile / 2, &qmap, 64, h * G, tok0 + qt[x].q0,
+                tma_tile_3d_g2s(dst + kQTile / 2, &qmap, 64, h * G, tok0 + qt[x].q0,
                                 &bars.q_full[x]);
             }
         };
@@ -197,11 +207,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             const int s = i % kStages;
             if (i >= kStages && !warp_wait(&bars.kv_empty[s], ((i - kStages) / kStages) & 1, p.status))
                 break;
+            // entry i: K for 0 and odd i, V for the others (the last one is a V)
+            const bool isv = i > 0 && ((i & 1) == 0 || i == 2 * ntiles - 1);
+            const int j = isv ? (i == 2 * ntiles - 1 ? ntiles - 1 : i / 2 - 1) : (i + 1) / 2;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars.kv_full[s], kTile);
-                const CUtensorMap *m = (i & 1) ? &vmap : &kmap;
+                const CUtensorMap *m = isv ? &vmap : &kmap;
                 const uint32_t dst = sbase + kOffKV + s * kTile;
-                const int tok = tok0 + (jbase + i / 2) * kKT;
+                const int tok = tok0 + (jbase + j) * kKT;
                 tma_tile_3d_g2s(dst, m, 0, h, tok, &bars.kv_full[s]);
                 tma_tile_3d_g2s(dst + kTile / 2, m, 64, h, tok, &bars.kv_full[s]);
             }
@@ -217,38 +230,49 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         for (int x = 0; x < 2; ++x)
             if (qt[x].ntiles > 0 && (x == 0 || issued > 0))
                 warp_wait(&bars.q_full[x], 0, nullptr);
-    } else if (warp == kWarpMma) {
-        // --------------------------------------------------- MMA issuer --
+    } else if (warp == kWarpQk) {
+        // ------------------------------------------------ Q K^T issuer --
         const uint64_t qd0 = desc_sw128(sbase + kOffQ, 16, 1024);
         const uint64_t kd0 = desc_sw128(sbase + kOffKV, 16, 1024);
-        const uint64_t vd0 = desc_sw128(sbase + kOffKV, kTile / 2, 1024);
-        // S_x = Q_x K(j)^T
-        auto qk = [&](int x, int j) -> bool {
-            const int i = 2 * j, s = i % kStages;
-            if (!warp_wait(&bars.kv_full[s], (i / kStages) & 1, p.status))
-                return false;
-            tc_fence_after();
-            const uint64_t qd = qd0 + (uint64_t)((x * kTile) >> 4);
+        bool ok = true;
+        for (int j = 0; ok && j < ntiles; ++j) {
+            const int i = k_entry(j), s = i % kStages;
             const uint64_t kd = kd0 + (uint64_t)((s * kTile) >> 4);
+            ok = warp_wait(&bars.kv_full[s], (i / kStages) & 1, p.status);
+            for (int x = 0; ok && x < 2; ++x) {
+                if (j >= qt[x].ntiles)
+                    continue;
+                // S_x(j - 1) is in registers
+                ok = j == 0 ? warp_wait(&bars.q_full[x], 0, p.status)
+                            : warp_wait(&bars.s_empty[x], (j - 1) & 1, p.status);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t qd = qd0 + (uint64_t)((x * kQTile) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint64_t o = (uint64_t)(((ks >> 2) * (kTile / 2) + (ks & 3) * 32) >> 4);
-                mma_f16_ss_elect(tmem + kTmS + x * 128, qd + o, kd + o, kIdescQK, ks > 0 ? 1u : 0u);
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_f16_ss_elect(
+                        tmem + kTmS + x * 128,
+                        qd + (uint64_t)(((ks >> 2) * (kQTile / 2) + (ks & 3) * 32) >> 4),
+                        kd + (uint64_t)(((ks >> 2) * (kTile / 2) + (ks & 3) * 32) >> 4), kIdescQK,
+                        ks > 0 ? 1u : 0u);
+                mma_commit_elect(&bars.s_full[x]);
             }
-            mma_commit_elect(&bars.s_full[x]);
-            // K(j)'s last user: B, or A where B does not reach it
-            if (x == 1 || j >= qt[1].ntiles)
+            if (ok)
                 mma_commit_elect(&bars.kv_empty[s]);
-            return true;
-        };
-        bool v_clean = false;
-        // O_x += P_x(j) V(j)
-        auto pv = [&](int x, int j) -> bool {
-            const int i = 2 * j + 1, s = i % kStages;
-            if (!warp_wait(&bars.kv_full[s], (i / kStages) & 1, p.status))
-                return false;
+        }
+        mma_commit_elect(&bars.mma_done[0]);
+        warp_wait(&bars.mma_done[0], 0, p.status);
+    } else if (warp == kWarpPv) {
+        // --------------------------------------------------- P V issuer --
+        const uint64_t vd0 = desc_sw128(sbase + kOffKV, kTile / 2, 1024);
+        bool ok = true;
+        for (int j = 0; ok && j < ntiles; ++j) {
+            const int i = v_entry(j), s = i % kStages;
+            const uint64_t vd = vd0 + (uint64_t)((s * kTile) >> 4);
+            ok = warp_wait(&bars.kv_full[s], (i / kStages) & 1, p.status);
             const int rows = len - (jbase + j) * kKT;   // of this sequence in the tile
-            if (rows < kKT && !v_clean) {
+            if (ok && rows < kKT) {
                 uint8_t *v = smem + kOffKV + s * kTile;
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                 for (int o = rows * 128 + lane * 16; o < kTile / 2; o += 512) {
@@ -257,46 +281,33 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                 }
                 fence_async_smem();
                 __syncwarp();
-                v_clean = true;
             }
-            const uint64_t vd = vd0 + (uint64_t)((s * kTile) >> 4);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!warp_wait(&bars.p_full[2 * x + half], j & 1, p.status))
-                    return false;
+            for (int x = 0; ok && x < 2; ++x) {
+                if (j >= qt[x].ntiles)
+                    continue;
+                ok = warp_wait(&bars.p_full[x], j & 1, p.status);
+                if (!ok)
+                    break;
                 tc_fence_after();
 #pragma unroll
-                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                    mma_f16_ts_elect(tmem + kTmO + x * 128, tmem + kTmS + x * 128 + ks * 8,
+                for (int ks = 0; ks < kKT / 16; ++ks)
+                    mma_f16_ts_elect(tmem + kTmO + x * 128, tmem + kTmP + x * 128 + ks * 8,
                                      vd + (uint64_t)((ks * 2048) >> 4), kIdescPV,
                                      (j > 0 || ks > 0) ? 1u : 0u);
-            }
-            if (j == qt[x].ntiles - 1)
                 mma_commit_elect(&bars.pv_done[x]);
-            if (x == 1 || j >= qt[1].ntiles)
+            }
+            if (ok)
                 mma_commit_elect(&bars.kv_empty[s]);
-            return true;
-        };
-        bool ok = true;
-        for (int x = 0; ok && x < 2; ++x)
-            if (qt[x].ntiles > 0)
-                ok = warp_wait(&bars.q_full[x], 0, p.status) && qk(x, 0);
-        for (int j = 0; ok && j < ntiles; ++j)
-            for (int x = 0; ok && x < 2; ++x)
-                if (j < qt[x].ntiles)
-                    // the next S overwrites this tile's P: the tensor core
-                    // executes a thread's MMAs in issue order
-                    ok = pv(x, j) && (j + 1 >= qt[x].ntiles || qk(x, j + 1));
-        mma_commit_elect(bars.mma_done);
-        warp_wait(bars.mma_done, 0, p.status);
-    }
+        }
+        mma_commit_elect(&bars.mma_done[1]);
+        warp_wait(&bars.mma_done[1], 0, p.status);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ------------------------------------------------------ softmax --
         const int x = warp >> 2;
         const int r = tid - 128 * x;         // row == TMEM lane
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t ts = tl + kTmS + x * 128, to = tl + kTmO + x * 128;
+        const uint32_t ts = tl + kTmS + x * 128, tp = tl + kTmP + x * 128;
+        const uint32_t to = tl + kTmO + x * 128;
         const QTile T = qt[x];
         const int pos = T.q0 + r / G;
         const bool valid = r < tpt * G && pos < len && T.ntiles > 0;
@@ -306,23 +317,28 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         float m_used = -INFINITY, l = 0.0f;   // m in units of the raw scores
         bool ok = true;
         for (int j = 0; j < T.ntiles; ++j) {
-            // S(j) complete also means P V of tile j-1 has completed (in-order MMAs)
             if (!warp_wait(&bars.s_full[x], j & 1, p.status)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             float v[kKT];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t ua[32], ub[32];
-                tmem_ld64(ts + 64 * q, ua, ub);
+            {
+                uint32_t ua[32], ub[32], uc[16];
+                tmem_ld80(ts, ua, ub, uc);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    v[64 * q + c] = __uint_as_float(ua[c]);
-                    v[64 * q + 32 + c] = __uint_as_float(ub[c]);
+                    v[c] = __uint_as_float(ua[c]);
+                    v[32 + c] = __uint_as_float(ub[c]);
                 }
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    v[64 + c] = __uint_as_float(uc[c]);
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.s_empty[x]);
             if (p.negate) {
 #pragma unroll
                 for (int c = 0; c < kKT; ++c)
@@ -335,16 +351,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                     if (key0 + c > pos || key0 + c < lo)
                         v[c] = -INFINITY;
             }
-            float m8[8];   // eight independent chains of three-input maxima
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m8[i] = fmaxf(v[i], v[i + 8]);
-#pragma unroll
-                for (int c = i + 16; c < kKT; c += 16)
-                    m8[i] = max3(m8[i], v[c], v[c + 8]);
+            const float mx = max3(max3(max16(v), max16(v + 16), max16(v + 32)), max16(v + 48),
+                                  max16(v + 64));
+            // P and O are free once P V of the previous tile has completed
+            if (j > 0 && !warp_wait(&bars.pv_done[x], (j - 1) & 1, p.status)) {
+                ok = false;
+                break;
             }
-            const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
-                                  fmaxf(m8[6], m8[7]));
+            tc_fence_after();
             // lazy rescale: only when the max grew by more than 2^8
             const bool need = m_used != -INFINITY && (mx - m_used) * kf > kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
@@ -370,31 +384,30 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int g = 0; g < kKT / 32; ++g) {
-                uint32_t pk[16];
+            for (int g = 0; g < kKT / 16; ++g) {
+                uint32_t pk[8];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const int cc = 32 * g + c;
+                for (int c = 0; c < 16; c += 2) {
+                    const int cc = 16 * g + c;
                     const float2 d = __ffma2_rn(make_float2(v[cc], v[cc + 1]), kf2, nm2);
                     const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                     acc[(c >> 1) & 3] = __fadd2_rn(acc[(c >> 1) & 3], e);
                     pk[c / 2] = pack2<BF>(e.x, e.y);
                 }
-                tmem_st16(ts + 16 * g, pk);
-                if (g & 1) {   // 64 keys of P
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&bars.p_full[2 * x + (g >> 1)]);
-                }
+                tmem_st8(tp + 8 * g, pk);
             }
             const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
             l += a.x + a.y;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.p_full[x]);
         }
 
         // ---- epilogue: O / l ----
-        const bool have_o = ok && T.ntiles > 0 && warp_wait(&bars.pv_done[x], 0, p.status);
+        const bool have_o =
+            ok && T.ntiles > 0 && warp_wait(&bars.pv_done[x], (T.ntiles - 1) & 1, p.status);
         if (have_o)
             tc_fence_after();
         const float f = have_o && l > 0.0f ? 1.0f / l : 0.0f;
@@ -423,7 +436,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     }
 
     __syncthreads();
-    if (warp == kWarpMma) {
+    if (warp == kWarpQk) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
