@@ -143,23 +143,26 @@ PKVQ_API pkvq_status pkvq_kv_write_quant(const pkvq_cache *cache, const void *k,
  * All fp32, division and product rounded to nearest, round() to the nearest
  * code, ties to even.  The value of a code is code * s.  Rows at or behind
  * context_lens[b] are left as they were.
- *   k, v            fp16 [cu[batch]][num_kv_heads][head_dim], 16-byte aligned,
+ *   k, v            fp16 [num_tokens][num_kv_heads][head_dim], 16-byte aligned,
  *                   sequences packed
+ *   num_tokens      rows of k and v, at least cu[batch] (a sequence whose rows
+ *                   would lie outside them is skipped)
  *   cu_seqlens_new  int32 [batch + 1], cu[0] = 0, nondecreasing; equal entries:
  *                   the sequence gets nothing
  *   block_table     int32 [batch][max_blocks_per_seq]
  *   context_lens    int32 [batch], the new tokens included
  *   max_new_len     host-side upper bound of n_b (sizes the launch)
  * A block that receives tokens must belong to one sequence of the call only.
- * batch == 0 or max_new_len == 0 is a no-op.  Other formats return
+ * batch, max_new_len or num_tokens of 0 is a no-op.  Other formats return
  * PKVQ_ERR_UNSUPPORTED, as pkvq_kv_write_quant does for these two (a token
  * alone does not say what its block's scale becomes).  Codes and scales are
  * bit-exact with the definition above.
  */
 PKVQ_API pkvq_status pkvq_kv_write_block_quant(const pkvq_cache *cache, const void *k, const void *v,
-                                const int32_t *cu_seqlens_new, const int32_t *block_table,
-                                int32_t max_blocks_per_seq, const int32_t *context_lens,
-                                int32_t batch, int32_t max_new_len, void *stream);
+                                int64_t num_tokens, const int32_t *cu_seqlens_new,
+                                const int32_t *block_table, int32_t max_blocks_per_seq,
+                                const int32_t *context_lens, int32_t batch,
+                                int32_t max_new_len, void *stream);
 
 /*
  * Workspace bytes pkvq_paged_attn_decode needs for this shape on the

@@ -141,7 +141,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.pkvq_kv_write_quant.restype = I32
     lib.pkvq_kv_write_quant.argtypes = [P, P, P, P, I32, P]
     lib.pkvq_kv_write_block_quant.restype = I32
-    lib.pkvq_kv_write_block_quant.argtypes = [P, P, P, P, P, I32, P, I32, I32, P]
+    lib.pkvq_kv_write_block_quant.argtypes = [P, P, P, ctypes.c_int64, P, P, I32, P, I32, I32, P]
     lib.pkvq_decode_weights_workspace_bytes.restype = SZ
     lib.pkvq_decode_weights_workspace_bytes.argtypes = [I32, I32, I32, I32, P]
     lib.pkvq_paged_attn_decode_weights.restype = I32
@@ -440,8 +440,10 @@ def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
     cs = cache.struct()
     dev = cache.k_cache.get_device()
     B, cols = _rows("context_lens", context_lens), _cols("block_table", block_table)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [tokens][num_kv_heads][head_dim]")
     rows = (k.shape[0], cs.num_kv_heads, cs.head_dim)
-    args = (_arg("k", k, torch.float16, rows, dev), _arg("v", v, torch.float16, rows, dev),
+    args = (_arg("k", k, torch.float16, rows, dev), _arg("v", v, torch.float16, rows, dev), rows[0],
             _arg("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev),
             _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
             _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_new_len))
@@ -519,7 +521,8 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
                               out: Optional[torch.Tensor] = None,
                               lse: Optional[torch.Tensor] = None,
                               workspace: Optional[torch.Tensor] = None, stream=None,
-                              sliding_window: int = 0) -> torch.Tensor:
+                              sliding_window: int = 0,
+                              query_pos: Optional[torch.Tensor] = None) -> torch.Tensor:
     """paged_attn_decode that also adds every key's softmax weight, summed over
     the query rows of its KV head, to weights fp32 [B][Hkv][>= max_context_len]
     (zero the entries of new tokens).  Input of kv_evict."""
@@ -537,7 +540,8 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
             need = decode_weights_workspace_bytes(cache, B, q_len, Hq, max_context_len)
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         ws, wbytes = _scratch(workspace, dev)
-        opts = _opts(sliding_window, None)
+        _arg("query_pos", query_pos, torch.int32, (B, q_len), dev)
+        opts = _opts(sliding_window, query_pos)
         _check(_lib().pkvq_paged_attn_decode_weights(
             ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
             _arg("out", out, torch.float16, shape, dev),

@@ -185,7 +185,7 @@ const char *pkvq_last_error(void)
 
 const char *pkvq_version(void)
 {
-    return "0.1.0";
+    return "0.2.0";
 }
 
 const char *pkvq_status_string(pkvq_status s)
@@ -267,9 +267,10 @@ bool block_write_grid_fits(const pkvq_cache *cache, int32_t batch, int32_t max_n
 }
 
 KvWriteBlockParams block_write_params(const pkvq_cache *cache, const void *k, const void *v,
-                                      const int32_t *cu_seqlens_new, const int32_t *block_table,
-                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
-                                      int32_t batch, int32_t max_new_len, uint32_t *status)
+                                      int64_t num_tokens, const int32_t *cu_seqlens_new,
+                                      const int32_t *block_table, int32_t max_blocks_per_seq,
+                                      const int32_t *context_lens, int32_t batch,
+                                      int32_t max_new_len, uint32_t *status)
 {
     KvWriteBlockParams p{};
     p.k_cache = static_cast<uint8_t *>(cache->k_cache);
@@ -278,6 +279,7 @@ KvWriteBlockParams block_write_params(const pkvq_cache *cache, const void *k, co
     p.v_scale_blk = cache->v_scale_blk;
     p.k = static_cast<const __half *>(k);
     p.v = static_cast<const __half *>(v);
+    p.num_tokens = num_tokens;
     p.cu_seqlens_new = cu_seqlens_new;
     p.block_table = block_table;
     p.context_lens = context_lens;
@@ -294,18 +296,19 @@ KvWriteBlockParams block_write_params(const pkvq_cache *cache, const void *k, co
 }  // namespace
 
 pkvq_status pkvq_kv_write_block_quant(const pkvq_cache *cache, const void *k, const void *v,
-                                      const int32_t *cu_seqlens_new, const int32_t *block_table,
-                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
-                                      int32_t batch, int32_t max_new_len, void *stream)
+                                      int64_t num_tokens, const int32_t *cu_seqlens_new,
+                                      const int32_t *block_table, int32_t max_blocks_per_seq,
+                                      const int32_t *context_lens, int32_t batch,
+                                      int32_t max_new_len, void *stream)
 {
     pkvq_status st = check_cache(cache);
     if (st != PKVQ_OK)
         return st;
     if (!kv_has_block_scale(cache->dtype))
         return PKVQ_ERR_UNSUPPORTED;   // pkvq_kv_write_quant
-    if (batch < 0 || max_new_len < 0 || max_blocks_per_seq < 0)
+    if (batch < 0 || max_new_len < 0 || max_blocks_per_seq < 0 || num_tokens < 0)
         return PKVQ_ERR_INVALID_ARG;
-    if (batch == 0 || max_new_len == 0)
+    if (batch == 0 || max_new_len == 0 || num_tokens == 0)
         return PKVQ_OK;
     if (!k || !v || !cu_seqlens_new || !block_table || !context_lens)
         return PKVQ_ERR_INVALID_ARG;
@@ -317,8 +320,8 @@ pkvq_status pkvq_kv_write_block_quant(const pkvq_cache *cache, const void *k, co
     if (!status)
         return PKVQ_ERR_CUDA;
     return from_cuda(launch_kv_write_block(
-        block_write_params(cache, k, v, cu_seqlens_new, block_table, max_blocks_per_seq,
-                           context_lens, batch, max_new_len, status),
+        block_write_params(cache, k, v, num_tokens, cu_seqlens_new, block_table,
+                           max_blocks_per_seq, context_lens, batch, max_new_len, status),
         cache->dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -419,8 +422,10 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
     p.scale_stride = scale_stride(cache);
     p.k_scale_tok = static_cast<const uint16_t *>(cache->k_scale_tok);
     p.v_scale_tok = static_cast<const uint16_t *>(cache->v_scale_tok);
-    p.k_scale_blk = cache->k_scale_blk;
-    p.v_scale_blk = cache->v_scale_blk;
+    // (the last fields of pkvq_cache are read for these formats only)
+    const bool blk_scale = kv_has_block_scale(cache->dtype);
+    p.k_scale_blk = blk_scale ? cache->k_scale_blk : nullptr;
+    p.v_scale_blk = blk_scale ? cache->v_scale_blk : nullptr;
     p.window = opts ? opts->sliding_window : 0;
     p.query_pos = opts ? opts->query_pos : nullptr;
     p.q = static_cast<const __half *>(q);
@@ -470,8 +475,8 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
             if (!block_write_grid_fits(cache, batch, q_len))
                 return PKVQ_ERR_UNSUPPORTED;
             const cudaError_t e = launch_kv_write_block(
-                block_write_params(cache, k_new, v_new, nullptr, block_table, max_blocks_per_seq,
-                                   context_lens, batch, q_len, p.status),
+                block_write_params(cache, k_new, v_new, (int64_t)batch * q_len, nullptr, block_table,
+                                   max_blocks_per_seq, context_lens, batch, q_len, p.status),
                 cache->dtype, st_);
             if (e != cudaSuccess)
                 return from_cuda(e);
@@ -602,8 +607,9 @@ pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights, int64_t
     p.v_cache = static_cast<uint8_t *>(cache->v_cache);
     p.k_scale_tok = static_cast<uint16_t *>(cache->k_scale_tok);
     p.v_scale_tok = static_cast<uint16_t *>(cache->v_scale_tok);
-    p.k_scale_blk = cache->k_scale_blk;
-    p.v_scale_blk = cache->v_scale_blk;
+    const bool blk_scale = kv_has_block_scale(cache->dtype);
+    p.k_scale_blk = blk_scale ? cache->k_scale_blk : nullptr;
+    p.v_scale_blk = blk_scale ? cache->v_scale_blk : nullptr;
     p.weights = weights;
     p.weight_stride = weight_stride;
     p.weights_out = weights_out;
@@ -745,8 +751,10 @@ pkvq_status pkvq_paged_attn_prefill_ex(const pkvq_cache *cache, const void *q, v
     p.k_scale = head_scale ? cache->k_scale : nullptr;
     p.v_scale = head_scale ? cache->v_scale : nullptr;
     p.scale_stride = scale_stride(cache);
-    p.k_scale_blk = cache->k_scale_blk;
-    p.v_scale_blk = cache->v_scale_blk;
+    // (the last fields of pkvq_cache are read for these formats only)
+    const bool blk_scale = kv_has_block_scale(cache->dtype);
+    p.k_scale_blk = blk_scale ? cache->k_scale_blk : nullptr;
+    p.v_scale_blk = blk_scale ? cache->v_scale_blk : nullptr;
     p.window = opts ? opts->sliding_window : 0;
     p.k_scale_tok = static_cast<const uint16_t *>(cache->k_scale_tok);
     p.v_scale_tok = static_cast<const uint16_t *>(cache->v_scale_tok);

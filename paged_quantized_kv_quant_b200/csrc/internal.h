@@ -52,7 +52,8 @@ cudaError_t launch_kv_write_quant(const KvWriteParams &p, int kv_dtype, cudaStre
 struct KvWriteBlockParams {
     uint8_t *k_cache, *v_cache;
     float *k_scale_blk, *v_scale_blk;      // [blocks][Hkv]
-    const __half *k, *v;                   // [tokens][Hkv][128]
+    const __half *k, *v;                   // [num_tokens][Hkv][128]
+    long long num_tokens;
     const int32_t *cu_seqlens_new;         // or null: q_len new tokens per sequence
     const int32_t *block_table, *context_lens;
     int max_blocks_per_seq, batch, max_new_len, q_len;

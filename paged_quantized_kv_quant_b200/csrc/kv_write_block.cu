@@ -90,6 +90,7 @@ kv_write_block_kernel(const KvWriteBlockParams p, const int max_touched)
             tok0 = __ldg(p.cu_seqlens_new + b);
             n = __ldg(p.cu_seqlens_new + b + 1) - tok0;
         }
+        act = tok0 >= 0 && tok0 + (long long)n <= p.num_tokens;   // rows that there are
     }
     const int start = ctx - n;          // position of the first new token (< 0: skipped)
     const int lo = max(start, 0);

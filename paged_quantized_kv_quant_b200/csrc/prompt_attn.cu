@@ -152,7 +152,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     // (never past the rows that there are)
     const int len = (int)min((long long)p.cu_seqlens[b + 1], p.total) - tok0;
     const int tpt = p.tokens_per_tile, G = p.group;
-    if (2 * pair * tpt >= len || device_wait_failed(p.status))
+    if (tok0 < 0 || 2 * pair * tpt >= len || device_wait_failed(p.status))
         return;
     const int jbase = p.window > 0 ? max(0, 2 * pair * tpt - p.window + 1) / kKT : 0;
     const QTile qt[2] = {make_qtile(2 * pair, tpt, len, jbase),

@@ -26,9 +26,9 @@ def cache(**kw):
 
 
 def write(lib, c, **kw):
-    a = dict(k=0x10000, v=0x20000, cu=0x30000, bt=0x40000, maxb=8, ctx=0x50000, B=2, n=4)
+    a = dict(k=0x10000, v=0x20000, T=8, cu=0x30000, bt=0x40000, maxb=8, ctx=0x50000, B=2, n=4)
     a.update(kw)
-    return lib.pkvq_kv_write_block_quant(ctypes.byref(c), P(a["k"]), P(a["v"]), P(a["cu"]), P(a["bt"]),
+    return lib.pkvq_kv_write_block_quant(ctypes.byref(c), P(a["k"]), P(a["v"]), a["T"], P(a["cu"]), P(a["bt"]),
                                          a["maxb"], P(a["ctx"]), a["B"], a["n"], None)
 
 
@@ -47,6 +47,8 @@ def test_block_write_refusals(lib):
     assert write(lib, cache(), B=1 << 20, n=1 << 20) == UNSUPPORTED    # the launch grid
     assert write(lib, cache(), n=(1 << 31) - 1, B=16) == UNSUPPORTED
     assert write(lib, cache(num_kv_heads=65536, num_blocks=1)) == UNSUPPORTED
+    assert write(lib, cache(), T=-1) == INVALID
+    assert write(lib, cache(), T=0, k=None) == OK
     assert write(lib, cache(), B=0, k=None) == OK
     assert write(lib, cache(), n=0, k=None) == OK
 
