@@ -447,6 +447,9 @@ pkvq_status decode_impl(const pkvq_cache *cache, const void *k_new, const void *
     p.num_splits = plan.num_splits;
     p.uniform_splits = plan.uniform_splits;
     p.uniform_bpc = plan.uniform_bpc;
+    p.uniform_more = plan.uniform_more;
+    p.uniform_bpc_more = plan.uniform_bpc_more;
+    p.spread = plan.spread;
     p.split_min_blocks = plan.split_min_blocks;
     p.split_gran = plan.split_gran;
     p.scale_log2 = softmax_scale * kLog2e;

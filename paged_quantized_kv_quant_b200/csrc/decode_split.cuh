@@ -488,8 +488,15 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
     // real assignment is computed from the context lengths, and reloaded
     // only when the guess was wrong (different lengths), so that with equal
     // lengths the first copies wait for one memory round trip, not two.
-    int b = min(slot / p.uniform_splits, p.batch - 1);
-    int blk_begin = (slot - b * p.uniform_splits) * p.uniform_bpc;
+    const int more = p.uniform_more * (p.uniform_splits + 1);   // slots of the sequences with one more
+    int b, blk_begin;
+    if (slot < more) {
+        b = slot / (p.uniform_splits + 1);
+        blk_begin = (slot - b * (p.uniform_splits + 1)) * p.uniform_bpc_more;
+    } else {
+        b = min(p.uniform_more + (slot - more) / p.uniform_splits, p.batch - 1);
+        blk_begin = (slot - more - (b - p.uniform_more) * p.uniform_splits) * p.uniform_bpc;
+    }
     const int h0 = h * p.group;
     int win0, win1;
     int win_base = 0;

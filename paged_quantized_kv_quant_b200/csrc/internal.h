@@ -88,6 +88,9 @@ struct DecodeParams {
                          // (sequence, split) on the device from the lengths
     int uniform_splits;  // splits per sequence when all hold max_context_len
     int uniform_bpc;     // blocks per split in that case
+    int uniform_more;    // sequences that have one split more in that case (spread)
+    int uniform_bpc_more;   // and their blocks per split
+    bool spread;         // left-over slots go to the first sequences
     int split_min_blocks, split_gran;   // shortest split; split sizes are multiples of gran
     float scale_log2;    // softmax_scale * log2(e)
     float *ws_o;         // [row groups x Hkv][C][rows_per_cta][128] fp32, unnormalised
@@ -107,6 +110,8 @@ struct DecodePlan {
     int rows_per_cta, row_groups;
     int num_splits;                     // C slots per (row group, KV head)
     int uniform_splits, uniform_bpc;    // the assignment with equal lengths
+    int uniform_more, uniform_bpc_more;
+    bool spread;
     int split_min_blocks, split_gran;
     bool tc;                            // tensor-core kernel: all rows of a KV head in one CTA
     size_t workspace_bytes;

@@ -41,6 +41,23 @@ __host__ __device__ inline int split_blocks(long long total, int C, int batch, i
     return (int)v;
 }
 
+// Spread calls (DecodeParams::spread) hand the slots that this leaves over, fewer
+// than one per sequence, to the first sequences long enough for one more split,
+// and even out every sequence's splits: with 8 equal sequences and 111 slots,
+// 13 splits of 160 blocks each (104 slots) become 14 of 147 for seven of them
+// and 13 of 158 for the last.  Blocks per split of a sequence of n blocks over ns
+// splits:
+__host__ __device__ inline int spread_blocks(int n, int ns, int gran)
+{
+    return ((n + ns - 1) / ns + gran - 1) / gran * gran;
+}
+
+// Whether n blocks over ns splits can take one more of at least min_blocks.
+__host__ __device__ inline bool spread_more(int n, int ns, int min_blocks)
+{
+    return n / (ns + 1) >= min_blocks;
+}
+
 struct SplitInfo {
     int b;        // sequence (-1: a slot past the last split)
     int split;    // split of that sequence
@@ -103,11 +120,33 @@ __device__ SplitInfo find_split(const DecodeParams &p, int slot, int seq)
                 split_blocks(total, p.num_splits, p.batch, longest, p.split_min_blocks,
                              p.split_gran),
                 0};
+    int spare = 0;
+    if (p.spread) {
+        int used = 0;
+        for (int base = 0; base < p.batch; base += 32) {
+            const int n = base == 0 ? n0 : seq_blocks<BS>(p, base + lane);
+            used += base + lane < p.batch ? max(1, (n + r.bpc - 1) / r.bpc) : 0;
+        }
+        spare = p.num_splits - __reduce_add_sync(0xffffffffu, used);
+    }
+    const int bpc = r.bpc;
     int run = 0;   // slots taken by the sequences before this chunk
     for (int base = 0; base < p.batch; base += 32) {
         const int i = base + lane;
         const int n = base == 0 ? n0 : seq_blocks<BS>(p, i);
-        const int ns = i < p.batch ? max(1, (n + r.bpc - 1) / r.bpc) : 0;
+        int ns = i < p.batch ? max(1, (n + bpc - 1) / bpc) : 0;
+        int mine = bpc;   // blocks per split of sequence i
+        if (p.spread) {
+            const bool more = n > 0 && spread_more(n, ns, p.split_min_blocks);
+            const unsigned em = __ballot_sync(0xffffffffu, more);
+            if (more && __popc(em & ((1u << lane) - 1u)) < spare)
+                ++ns;
+            spare -= __popc(em);
+            if (n > 0) {
+                mine = spread_blocks(n, ns, p.split_gran);
+                ns = (n + mine - 1) / mine;
+            }
+        }
         int incl = ns;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -124,6 +163,7 @@ __device__ SplitInfo find_split(const DecodeParams &p, int slot, int seq)
             r.b = base + src;
             r.first = __shfl_sync(0xffffffffu, first, src);
             r.nsplit = __shfl_sync(0xffffffffu, ns, src);
+            r.bpc = __shfl_sync(0xffffffffu, mine, src);
             r.split = slot >= 0 ? slot - r.first : 0;
             r.ctx = max(p.context_lens[r.b], 0);
             r.blk0 = seq_first_block<BS>(p, r.b, r.ctx);
