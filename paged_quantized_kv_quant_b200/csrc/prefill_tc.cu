@@ -10,30 +10,31 @@
 // A CTA owns two adjacent query tiles A and B of 128 rows each (a tile is
 // 128/G query tokens x the G query heads of one KV head).  Both tiles read the
 // same keys, so every 64-key tile is fetched and dequantised once for 256
-// query rows.  Q and P are kept in tensor memory, so the MMAs read only the
-// fp16 K/V tiles from shared memory (operand bandwidth, not arithmetic, is
-// what bounds a 128 x 64 product).  Warp roles (12 warps):
-//   warps 0-1   dequant: E4M3/int8 code tiles -> fp16 K and V tiles in the
-//               128-byte-swizzled canonical layout [d half][key][64 d].  The
-//               same bytes are the K-major B operand of S = Q K^T and the
-//               MN-major B operand of O = P V, so V is never transposed.
-//   warp 2      TMA producer: one 2-D tensor copy per cache block and head
-//               into a 3-stage code ring; block ids come from a register window.
-//   warp 3      allocates all 512 TMEM columns (per tile: S/P 64, O 128, Q 64)
-//               and issues every MMA: the whole warp runs the loop on
-//               warp-uniform values and an elected lane issues each tcgen05
-//               instruction.  It serves whichever tile has its P ready
-//               (O += P V, then S = Q K_next in the same columns), sleeping
-//               with a bounded mbarrier wait on the tile that is due.
-//               Completion is signalled with tcgen05.commit on mbarriers.
+// query rows.  Tensor memory holds, per query tile, S (64 columns), P (32) and O
+// (128), all apart: S(j+1) = Q K(j+1)^T is issued as soon as the softmax has
+// S(j) in registers, so a tile's softmax does not wait for the tensor core.  (With
+// P written over S, and Q in tensor memory instead of shared memory, every S
+// waited for its tile's P V: a 2K chunk over 30K of block-scaled E4M3 took 1.40
+// instead of 1.25 ms, the 8K prompt 0.616 instead of 0.574 ms; same bits.)
+// Warp roles (16 warps; warpgroups 0 and 3 give registers to the softmax):
+//   warps 0-1, 12-13  dequant: E4M3/int8 code tiles -> fp16 K (warps 0-1) and V
+//               tiles in the 128-byte-swizzled canonical layout [d half][key]
+//               [64 d].  The same bytes are the K-major B operand of S = Q K^T and
+//               the MN-major B operand of O = P V, so V is never transposed.
+//   warp 2      copies: the cache blocks of a tile into a 3-stage code ring;
+//               block ids come from a register window.
+//   warp 3      allocates all 512 TMEM columns and issues S = Q K^T, warp 14 O +=
+//               P V (a thread's tcgen05.mma returns only once the tensor core has
+//               taken it, so one issuer would queue each behind the other): the
+//               whole warp runs the loop on warp-uniform values and an elected
+//               lane issues each instruction.  Completion is signalled with
+//               tcgen05.commit on mbarriers.
 //   warps 4-7   softmax for tile A, warps 8-11 softmax for tile B: thread i of
-//               a group owns row i (TMEM lane i): it stores its Q row in TMEM,
-//               reads its S row, masks only on tiles that cross the diagonal,
-//               keeps the FP32 running max/sum in registers, writes its fp16 P
-//               row over the S columns it came from, and rescales its O row in
-//               TMEM only when the row maximum grew by more than 2^8.  The
-//               tensor core runs one group's products while the other group's
-//               softmax runs.
+//               a group owns row i (TMEM lane i): it puts its Q row into shared
+//               memory, reads its S row, masks only on tiles that cross the
+//               diagonal, keeps the FP32 running max/sum in registers, writes its
+//               fp16 P row, and rescales its O row in TMEM only when the row
+//               maximum grew by more than 2^8.
 //
 // Block-scaled formats (a K and a V scale per block and KV head): the dequant
 // warps hand the softmax three factors for each 16 keys, and the softmax takes
@@ -58,10 +59,12 @@
 namespace pkvq {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kKT = 64;              // keys per tile
 constexpr int kCodeStages = 3;
-constexpr int kKVBufs = 4;           // dequantised K/V tiles in flight
+// dequantised K/V tiles in flight (FP16 caches are copied straight into them)
+template <int KVT>
+constexpr int kKVBufsOf = KVT == kKvFp16 ? 4 : 3;
 // L2 prefetch distance in tiles: with 16-token blocks the farthest prefetched
 // block stays within 60 entries of the block-table window's base
 constexpr int kPrefetchTiles = 6;
@@ -69,27 +72,34 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by > 2^8
 
 constexpr int kWarpTma = 2;
-constexpr int kWarpMma = 3;
-constexpr int kDequantWarps = 2;
+constexpr int kWarpQk = 3;
+constexpr int kWarpPv = 14;
+constexpr int kDequantWarps = 4;     // 0, 1 (K), 12, 13 (V)
 
-// tensor memory, per query tile x at x * 256: S/P (P in the first 32), O, Q
-constexpr uint32_t kTmS = 0, kTmO = 64, kTmQ = 192;
+// tensor memory, per query tile x at x * 256
+constexpr uint32_t kTmS = 0, kTmP = 64, kTmO = 128;
 
 // shared-memory map (offsets from a 1024-byte aligned base)
-constexpr int kOffKV = 0;                                 // bufs x (K 8K+8K, V 8K+8K)
 constexpr int kKVBuf = 32768;
-constexpr int kOffCodes = kOffKV + kKVBufs * kKVBuf;      // stages x (K 8K, V 8K)
 constexpr int kCodeStage = 16384;
-constexpr int kOffScl = kOffCodes + kCodeStages * kCodeStage;   // stages x (K 64, V 64) halves
-constexpr int kOffKsf = kOffScl + kCodeStages * 256;            // bufs x 64 fp32 K factors
-// (block-scaled formats: per buffer, 4 x ks, 4 x lv, 4 x iv of its four 16-key
-// groups, see BlockFactors, at the start of its 64)
-constexpr int kOffBars = kOffKsf + kKVBufs * 64 * 4;
-constexpr int kNumBars = 1 + 2 * kCodeStages + 3 * kKVBufs + 3 * 2 + 1;
-constexpr int kOffTaddr = kOffBars + kNumBars * 8;
-constexpr int kSmemBytes = kOffTaddr + 16;
-constexpr size_t kSmemAlloc = kSmemBytes + 1024;
-static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
+constexpr int kQTile = 32768;                             // two 64-wide halves of 128 rows
+template <int KVT>
+struct Smem {
+    static constexpr int kKVBufs = kKVBufsOf<KVT>;
+    static constexpr int kQ = 0;                                  // 2 query tiles
+    static constexpr int kKV = 2 * kQTile;                        // bufs x (K 8K+8K, V 8K+8K)
+    static constexpr int kCodes = kKV + kKVBufs * kKVBuf;         // stages x (K 8K, V 8K)
+    static constexpr int kScl =                                   // stages x (K 64, V 64) halves
+        kCodes + (KVT == kKvFp16 ? 0 : kCodeStages * kCodeStage);
+    static constexpr int kKsf = kScl + kCodeStages * 256;         // bufs x 64 fp32 K factors
+    // (block-scaled formats: per buffer, 4 x ks, 4 x lv, 4 x iv of its four 16-key
+    // groups, see BlockFactors, at the start of its 64)
+    static constexpr int kBars = kKsf + kKVBufs * 64 * 4;
+    static constexpr int kNumBars = 1 + 2 * kCodeStages + 3 * kKVBufs + 4 * 2 + 2;
+    static constexpr int kTaddr = kBars + kNumBars * 8;
+    static constexpr size_t kAlloc = kTaddr + 16 + 1024;
+    static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
 
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, kKT, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 128, true);
@@ -98,25 +108,28 @@ struct Bars {
     uint64_t *q_full;
     uint64_t *code_full, *code_empty;   // [kCodeStages]
     uint64_t *kv_full, *kv_empty;       // [kKVBufs]
-    uint64_t *s_full, *p_full, *pv_done;   // [tile]
-    uint64_t *mma_done;                 // all MMAs retired (before TMEM is freed)
+    uint64_t *s_full, *s_empty;         // [tile] S written / in registers
+    uint64_t *p_full, *pv_done;         // [tile]
+    uint64_t *mma_done;                 // [issuer] its MMAs retired (before TMEM is freed)
     uint64_t *kv_tma;                   // [kKVBufs] FP16: the buffer's copies landed
 };
 
+template <int KVT>
 __device__ __forceinline__ Bars carve_bars(uint8_t *smem)
 {
-    uint64_t *b = reinterpret_cast<uint64_t *>(smem + kOffBars);
+    uint64_t *b = reinterpret_cast<uint64_t *>(smem + Smem<KVT>::kBars);
     Bars r;
     r.q_full = b;
     r.code_full = b + 1;
     r.code_empty = r.code_full + kCodeStages;
     r.kv_full = r.code_empty + kCodeStages;
-    r.kv_empty = r.kv_full + kKVBufs;
-    r.s_full = r.kv_empty + kKVBufs;
-    r.p_full = r.s_full + 2;
+    r.kv_empty = r.kv_full + kKVBufsOf<KVT>;
+    r.s_full = r.kv_empty + kKVBufsOf<KVT>;
+    r.s_empty = r.s_full + 2;
+    r.p_full = r.s_empty + 2;
     r.pv_done = r.p_full + 2;
     r.mma_done = r.pv_done + 2;
-    r.kv_tma = r.mma_done + 1;
+    r.kv_tma = r.mma_done + 2;
     return r;
 }
 
@@ -176,14 +189,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const PrefillParams p)
 {
+    using M = Smem<KVT>;
+    constexpr int kKVBufs = M::kKVBufs;
+    constexpr int kOffKV = M::kKV, kOffCodes = M::kCodes, kOffScl = M::kScl, kOffKsf = M::kKsf;
     constexpr int kBPT = kKT / BS;   // cache blocks per key tile
     static_assert((kPrefetchTiles + 1) * kBPT <= 32, "prefetches stay in the table window");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    Bars bars = carve_bars(smem);
-    uint32_t *taddr_smem = reinterpret_cast<uint32_t *>(smem + kOffTaddr);
+    Bars bars = carve_bars<KVT>(smem);
+    uint32_t *taddr_smem = reinterpret_cast<uint32_t *>(smem + M::kTaddr);
 
     const int npairs = (p.q_tiles + 1) / 2;
     const int pair = npairs - 1 - blockIdx.x;   // longest causal work first
@@ -219,13 +235,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.s_empty[i], 4);
             mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.pv_done[i], 1);
+            mbar_init(&bars.mma_done[i], 1);
         }
-        mbar_init(bars.mma_done, 1);
         fence_mbar_init();
     }
-    if (warp == kWarpMma) {
+    if (warp == kWarpQk) {
         tmem_alloc(taddr_smem, 512);
         tmem_relinquish();
         tc_fence_before();
@@ -234,6 +251,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     tc_fence_after();
     const uint32_t tmem = *taddr_smem;
 
+    // 512 x 128 registers at launch: 256 x 64 + 256 x 184 fit in them
+    if (warp < 4 || warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kWarpTma) {
         // ---------------------------------------------- copy producer --
         // 16-byte cp.async copies by all 32 lanes; each lane arrives on the
@@ -280,110 +300,76 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         // copies this warp issued land before it exits
         cp_async_wait_all();
-    } else if (warp == kWarpMma) {
-        // --------------------------------------------------- MMA issuer --
-        // Serves whichever query tile has its P ready (no head-of-line
-        // blocking between the two softmax groups); a K/V buffer is released
-        // once every tile that uses it has issued its P V product.  The whole
-        // warp runs this loop on warp-uniform values (every wait and probe is
-        // made uniform by a vote) and one elected lane issues each tcgen05
-        // instruction.
+    } else if (warp == kWarpQk) {
+        // ------------------------------------------------ Q K^T issuer --
         if (ntiles > 0) {
             bool ok = warp_wait(bars.q_full, 0, p.status);
-            tc_fence_after();
-            // descriptors of K/V buffer 0; buffer b adds b * kKVBuf bytes
+            // descriptors of query tile 0 and K/V buffer 0
+            const uint64_t qd0 = desc_sw128(sbase + M::kQ, 16, 1024);
             const uint64_t kd0 = desc_sw128(sbase + kOffKV, 16, 1024);
-            const uint64_t vd0 = desc_sw128(sbase + kOffKV + 16384, 8192, 1024);
-            auto qk = [&](int x, int j) -> bool {   // S_x = Q_x K(j)^T
+            for (int j = 0; ok && j < ntiles; ++j) {
                 const int kvb = j % kKVBufs;
-                if (!warp_wait(&bars.kv_full[kvb], (j / kKVBufs) & 1, p.status))
-                    return false;
-                tc_fence_after();
-                const uint32_t tx = tmem + x * 256;
                 const uint64_t kd = kd0 + (uint64_t)((kvb * kKVBuf) >> 4);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_f16_ts_elect(tx + kTmS, tx + kTmQ + ks * 8,
-                                     kd + (uint64_t)(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
-                                     kIdescQK, ks > 0 ? 1u : 0u);
-                mma_commit_elect(&bars.s_full[x]);
-                return true;
-            };
-            auto pv = [&](int x, int j) {   // O_x += P_x(j) V(j); P_x(j) is ready
-                tc_fence_after();
-                const uint32_t tx = tmem + x * 256;
-                const uint64_t vd = vd0 + (uint64_t)(((j % kKVBufs) * kKVBuf) >> 4);
-#pragma unroll
-                for (int ks = 0; ks < kKT / 16; ++ks)
-                    mma_f16_ts_elect(tx + kTmO, tx + kTmS + ks * 8,
-                                     vd + (uint64_t)((ks * 2048) >> 4), kIdescPV,
-                                     (j > 0 || ks > 0) ? 1u : 0u);
-                mma_commit_elect(&bars.pv_done[x]);
-            };
-            for (int x = 0; ok && x < 2; ++x)
-                if (qt[x].ntiles > 0 && !qk(x, 0))
-                    ok = false;
-            int nxt[2] = {0, 0};   // next P V tile of each query tile
-            int released = 0;      // K/V tiles released so far
-            // The warp sleeps (bounded, kPollSleepNs) on the barrier of the tile
-            // whose P is due first, so it neither spins on issue slots the
-            // softmax warps of its scheduler need nor reacts late to that
-            // tile; the other tile is then probed without blocking.  The clock
-            // is read every 16 idle rounds.
-            constexpr uint32_t kPollSleepNs = 200;
-            uint64_t t_last = 0;
-            uint32_t idle = 0;
-            while (ok && (nxt[0] < qt[0].ntiles || nxt[1] < qt[1].ntiles)) {
-                bool progressed = false;
-                // the tile due first: fewer P V products issued (A on ties)
-                const int xd = (nxt[0] < qt[0].ntiles &&
-                                (nxt[0] <= nxt[1] || nxt[1] >= qt[1].ntiles)) ? 0 : 1;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int x = xd ^ k;
-                    const int j = nxt[x];
+                ok = warp_wait(&bars.kv_full[kvb], (j / kKVBufs) & 1, p.status);
+                for (int x = 0; ok && x < 2; ++x) {
                     if (j >= qt[x].ntiles)
                         continue;
-                    const bool rdy = k == 0
-                                         ? mbar_try_wait_for(&bars.p_full[x], j & 1, kPollSleepNs)
-                                         : mbar_test_wait(&bars.p_full[x], j & 1);
-                    if (!__any_sync(0xffffffffu, rdy))
-                        continue;
-                    pv(x, j);
-                    nxt[x] = j + 1;
-                    progressed = true;
-                    // The next S overwrites this tile's P in the same columns;
-                    // the tensor core executes a thread's MMAs in issue order.
-                    if (j + 1 < qt[x].ntiles && !qk(x, j + 1)) {
+                    // S_x(j - 1) is in registers
+                    if (j > 0 && !warp_wait(&bars.s_empty[x], (j - 1) & 1, p.status)) {
                         ok = false;
                         break;
                     }
-                }
-                while (released < ntiles && (released >= qt[0].ntiles || nxt[0] > released) &&
-                       (released >= qt[1].ntiles || nxt[1] > released)) {
-                    mma_commit_elect(&bars.kv_empty[released % kKVBufs]);
-                    ++released;
-                }
-                if (progressed) {
-                    idle = 0;
-                } else if ((++idle & 15u) == 0) {
-                    // lane 0's clock decides, so that the warp stays converged
-                    const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
-                    if (idle == 16u) {
-                        t_last = now;   // first check of this idle stretch
-                    } else if (now - t_last > kWaitLimitNs) {
-                        if (lane == 0)
-                            atomicOr(p.status, kStatusWaitTimeout);
-                        ok = false;
-                    }
+                    tc_fence_after();
+                    const uint64_t qd = qd0 + (uint64_t)((x * kQTile) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_f16_ss_elect(
+                            tmem + x * 256 + kTmS,
+                            qd + (uint64_t)(((ks >> 2) * (kQTile / 2) + (ks & 3) * 32) >> 4),
+                            kd + (uint64_t)(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), kIdescQK,
+                            ks > 0 ? 1u : 0u);
+                    mma_commit_elect(&bars.s_full[x]);
                 }
             }
-            mma_commit_elect(bars.mma_done);
-            warp_wait(bars.mma_done, 0, p.status);
+            mma_commit_elect(&bars.mma_done[0]);
+            warp_wait(&bars.mma_done[0], 0, p.status);
         }
-    } else if (warp < kDequantWarps) {
+    } else if (warp == kWarpPv) {
+        // --------------------------------------------------- P V issuer --
+        // P_x(j) followed S_x(j), which followed K(j) and V(j) (one barrier for
+        // both halves of the buffer).  Its commit releases the buffer: each Q K^T
+        // on it completed before the P V of the same tile was issued.
+        if (ntiles > 0) {
+            bool ok = true;
+            const uint64_t vd0 = desc_sw128(sbase + kOffKV + 16384, 8192, 1024);
+            for (int j = 0; ok && j < ntiles; ++j) {
+                const int kvb = j % kKVBufs;
+                const uint64_t vd = vd0 + (uint64_t)((kvb * kKVBuf) >> 4);
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (j >= qt[x].ntiles)
+                        continue;
+                    ok = warp_wait(&bars.p_full[x], j & 1, p.status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t tx = tmem + x * 256;
+#pragma unroll
+                    for (int ks = 0; ks < kKT / 16; ++ks)
+                        mma_f16_ts_elect(tx + kTmO, tx + kTmP + ks * 8,
+                                         vd + (uint64_t)((ks * 2048) >> 4), kIdescPV,
+                                         (j > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit_elect(&bars.pv_done[x]);
+                }
+                if (ok)
+                    mma_commit_elect(&bars.kv_empty[kvb]);
+            }
+            mma_commit_elect(&bars.mma_done[1]);
+            warp_wait(&bars.mma_done[1], 0, p.status);
+        }
+    } else if (warp < 2 || warp == 12 || warp == 13) {
         // ------------------------------------------------------ dequant --
-        const int row = tid;   // 0..63: this thread converts key row `row` of K and V
+        const int isv = warp >= 12;
+        const int row = tid & 63;   // this thread converts key row `row` of K or of V
         const float kfac = p.scale_log2;
         if constexpr (KVT == kKvFp16) {
             // clear the rows past the context, then release the buffer
@@ -392,10 +378,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (!warp_wait(&bars.kv_tma[bj], (j / kKVBufs) & 1, p.status))
                     break;
                 if ((jbase + j) * kKT + row >= ctx) {
-                    uint8_t *kv = smem + kOffKV + bj * kKVBuf;
+                    uint8_t *kv = smem + kOffKV + bj * kKVBuf + isv * 16384;
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int hh = 0; hh < 4; ++hh)   // K d halves 0, 1, V d halves 0, 1
+                    for (int hh = 0; hh < 2; ++hh)   // d halves
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             *reinterpret_cast<uint4 *>(kv + hh * 8192 + row * 128 + c * 16) = z;
@@ -418,9 +404,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             uint8_t *kv = smem + kOffKV + bj * kKVBuf;
             const int key0 = (jbase + j) * kKT;
 #pragma unroll 4
-            for (int k = 0; k < 16; ++k) {
-                const int isv = k >> 3;
-                const int cc = k & 7;   // 16-byte code chunk
+            for (int cc = 0; cc < 8; ++cc) {   // 16-byte code chunk
                 const uint4 w = *reinterpret_cast<const uint4 *>(codes + isv * 8192 + swz(row, cc));
                 uint32_t hv[8];
                 cvt4<KVT>(w.x, hv[0], hv[1]);
@@ -450,14 +434,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 *reinterpret_cast<uint4 *>(dst + swz(row, (2 * cc + 1) & 7)) =
                     make_uint4(hv[4], hv[5], hv[6], hv[7]);
             }
-            if constexpr (KVT == kKvInt8) {
+            if (KVT == kKvInt8 && !isv) {
                 // per-key score factor: softmax scale * log2(e) * K scale
                 float *ksf = reinterpret_cast<float *>(smem + kOffKsf) + bj * 64;
                 ksf[row] =
                     key0 + row < ctx ? kfac * __half2float(__ushort_as_half(scl[row])) : 0.0f;
             }
             if constexpr (kv_has_block_scale(KVT)) {
-                if ((row & 15) == 0) {
+                if (!isv && (row & 15) == 0) {
                     const float *sb = reinterpret_cast<const float *>(scl) + row / BS;
                     const BlockFactors f(kfac, sb[0], sb[4], key0 + row < ctx);
                     float *dst = reinterpret_cast<float *>(smem + kOffKsf) + bj * 64 + row / 16;
@@ -471,7 +455,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 mbar_arrive(&bars.kv_full[bj]);
             }
         }
-    } else if (warp >= 4) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------------------ softmax --
         const int x = (warp - 4) >> 2;       // query tile of this group
         const int r = tid - 128 - 128 * x;   // row == TMEM lane
@@ -483,21 +469,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const int pos = ctx - q_len + tq;
         const size_t qrow = (size_t)(q_start + tq) * p.num_q_heads + (size_t)h * G + gq;
 
-        // Q row -> tensor memory (two fp16 per column), zeros for padding rows
+        // Q row -> shared memory (K-major A operand), zeros for padding rows
         {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + qrow * kHeadDim);
+            uint8_t *dst = smem + M::kQ + x * kQTile;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t w[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 v = valid ? __ldg(src + half * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-                    w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
-                }
-                tmem_st32(tl + kTmQ + 32 * half, w);
-            }
-            tmem_st_wait();
-            tc_fence_before();
+            for (int c = 0; c < 16; ++c)
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kQTile / 2) + swz(r, c & 7)) =
+                    valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            fence_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bars.q_full);
@@ -512,7 +492,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         float m_used = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < T.ntiles; ++j) {
-            // S(j) complete also means P V of tile j-1 has completed (in-order MMAs)
             if (!warp_wait(&bars.s_full[x], j & 1, p.status)) {
                 ok = false;
                 break;
@@ -535,6 +514,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     v[32 + c] = __uint_as_float(ub[c]);
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.s_empty[x]);
 
             const int key0 = (jbase + j) * kKT;
             float bks[4], blv[4], biv[4];
@@ -591,6 +574,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                            fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
             }
+            // P and O are free once P V of the previous tile has completed
+            if (j > 0 && !warp_wait(&bars.pv_done[x], (j - 1) & 1, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
             // lazy rescale: only when the max grew by more than 2^8
             const bool need = m_used != -INFINITY && mx > m_used + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
@@ -641,8 +630,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 const float2 a = __fadd2_rn(a01, a23);
                 l += a.x + a.y;
             }
-            // P row over the first 32 S columns (the A operand of P V)
-            tmem_st32(tl + kTmS, pk);
+            tmem_st32(tl + kTmP, pk);   // the A operand of P V
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -686,7 +674,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     }
 
     __syncthreads();
-    if (warp == kWarpMma) {
+    if (warp == kWarpQk) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -697,12 +685,13 @@ cudaError_t launch_tc(const PrefillParams &p, const CUtensorMap &kmap, const CUt
                       cudaStream_t stream)
 {
     auto kern = prefill_tc_kernel<KVT, BS>;
+    constexpr size_t smem = Smem<KVT>::kAlloc;
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemAlloc);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
     dim3 grid((p.q_tiles + 1) / 2, p.num_kv_heads, p.batch);
-    kern<<<grid, kThreads, kSmemAlloc, stream>>>(kmap, vmap, p);
+    kern<<<grid, kThreads, smem, stream>>>(kmap, vmap, p);
     return cudaGetLastError();
 }
 
