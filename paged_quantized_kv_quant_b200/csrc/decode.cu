@@ -61,7 +61,12 @@ bool decode_plan(int kv_dtype, int batch, int q_len, int num_q_heads, int num_kv
     const int units = num_kv_heads * plan->row_groups;   // grid y: (row group, KV head)
     // splits: tensor-core kernel in whole 64-key tiles, at least 256 keys;
     // mma.sync kernel at least kMinBlocksPerWarp blocks per warp
-    const int min_blocks = plan->tc ? 256 / block_size : kWarps * kMinBlocksPerWarp;
+    // (block-scaled formats and calls with weights: one loop iteration per warp, 2
+    // blocks of 16 tokens or one larger; a short sequence then takes more CTAs)
+    const bool fine = weights || kv_has_block_scale(kv_dtype);
+    const int min_blocks = plan->tc ? 256 / block_size
+                           : !fine  ? kWarps * kMinBlocksPerWarp
+                                    : kWarps * (block_size == 16 ? 2 : 1);
     plan->split_min_blocks = min_blocks;
     plan->split_gran = plan->tc ? 64 / block_size : 1;
     // C CTA slots per unit, at most `ctas_per_sm` CTAs on every SM (3, or

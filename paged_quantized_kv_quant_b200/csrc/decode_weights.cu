@@ -22,10 +22,14 @@ constexpr int kWThreads = 256;
 // four CTAs per SM they run at once (2, 4 or 8 keys per thread with 5, 3 or 2 CTAs
 // per SM: the whole call takes 45.2, 42.6 or 40.5 us, with 4 and 4 40.7 us).
 constexpr int kKeysPerThread = 4;
-constexpr int kChunk = kWThreads * kKeysPerThread;
+// Keys per CTA.  With more than 8 score rows a key's scores are spread over the
+// lanes of a warp instead (a thread that walks 120 rows of its own key alone made
+// 40 of 61 us of a 15-token, 8-head call over 1,120 keys), and a CTA takes fewer.
+template <int RR>
+constexpr int kChunkOf = RR ? kWThreads * kKeysPerThread : 128;
 constexpr int kMaxRows = 256;   // 16 query tokens x 16 heads per KV head
 
-// Grid: x < chunks: keys [x * kChunk, ...) of (KV head y, sequence z); the
+// Grid: x < chunks: keys [x * kChunkOf<RR>, ...) of (KV head y, sequence z); the
 // remaining CTAs merge the partial states of 8 output rows each.
 // RR: score rows per key (1, 2, 4, 8), or 0 for any multiple of 4.
 template <int BS, int RR>
@@ -58,6 +62,7 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
     const int R = RR ? RR : p.score_rows;
     const int lo = si.blk0 * BS;   // scores exist for keys lo .. ctx - 1
     const int hi = min(si.ctx, min(p.score_keys, (int)min(p.weight_stride, (long long)INT_MAX)));
+    constexpr int kChunk = kChunkOf<RR>;
     const int c0 = blockIdx.x * kChunk;
     if (c0 >= hi || c0 + kChunk <= lo)
         return;   // (a CTA-wide decision)
@@ -66,9 +71,10 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
 
     // this thread's scores and weights are on their way while the row
     // normalisers are combined
-    float v[kKeysPerThread][RR ? RR : 1], w[kKeysPerThread];
+    constexpr int kKeys = RR ? kKeysPerThread : 1;
+    float v[kKeys][RR ? RR : 1], w[kKeys];
 #pragma unroll
-    for (int k = 0; k < kKeysPerThread; ++k) {
+    for (int k = 0; k < (RR ? kKeys : 0); ++k) {
         const int key = c0 + k * kWThreads + threadIdx.x;
         w[k] = 0.0f;
         if (key >= lo && key < hi) {
@@ -89,14 +95,15 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
             }
         }
     }
-    // log2-sum-exp2 of every row from its splits' (max, sum) states; rows
-    // that see no key (and padding rows) get +inf: weight 0
-    for (int r = warp; r < R; r += kWThreads / 32) {
-        float M = -INFINITY, L = 0.0f;
+    // log2-sum-exp2 of every row from its splits' (max, sum) states, all rows at
+    // once: a warp per row for up to 8 rows, otherwise `lp` lanes (a power of
+    // two); rows that see no key (and padding rows) get +inf: weight 0
+    auto row_state = [&](int r, int sub, int lp, float &M, float &L) {
+        M = -INFINITY, L = 0.0f;
         if (r < p.rows) {
             const size_t row0 = (size_t)((r / p.rows_per_cta) * p.num_kv_heads + h) *
                                     p.num_splits * p.rows_per_cta + r % p.rows_per_cta;
-            for (int s = lane; s < si.nsplit; s += 32) {
+            for (int s = sub; s < si.nsplit; s += lp) {
                 const float2 ml = *reinterpret_cast<const float2 *>(
                     p.ws_ml + (row0 + (size_t)(si.first + s) * p.rows_per_cta) * 2);
                 const float m = fmaxf(M, ml.x), mu = m == -INFINITY ? 0.0f : m;
@@ -104,44 +111,91 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
                 M = m;
             }
         }
+    };
+    auto join = [&](int o, float &M, float &L) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, M, o);
+        const float l2 = __shfl_xor_sync(0xffffffffu, L, o);
+        const float m = fmaxf(M, m2), mu = m == -INFINITY ? 0.0f : m;
+        L = L * fast_exp2(M - mu) + l2 * fast_exp2(m2 - mu);
+        M = m;
+    };
+    float M, L;
+    if constexpr (RR != 0) {
+        for (int r = warp; r < RR; r += kWThreads / 32) {
+            row_state(r, lane, 32, M, L);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, M, o);
-            const float l2 = __shfl_xor_sync(0xffffffffu, L, o);
-            const float m = fmaxf(M, m2), mu = m == -INFINITY ? 0.0f : m;
-            L = L * fast_exp2(M - mu) + l2 * fast_exp2(m2 - mu);
-            M = m;
+            for (int o = 16; o > 0; o >>= 1)
+                join(o, M, L);
+            if (lane == 0)
+                lse2[r] = L > 0.0f ? M + log2f(L) : INFINITY;
         }
-        if (lane == 0)
+    } else {
+        int lp = 32;
+        while (kWThreads / lp < R)
+            lp /= 2;
+        const int r = threadIdx.x / lp, sub = threadIdx.x % lp;
+        row_state(r, sub, lp, M, L);
+        for (int o = lp / 2; o > 0; o >>= 1)
+            join(o, M, L);
+        if (sub == 0 && r < R)
             lse2[r] = L > 0.0f ? M + log2f(L) : INFINITY;
     }
     __syncthreads();
+    if constexpr (RR != 0) {
 #pragma unroll
-    for (int k = 0; k < kKeysPerThread; ++k) {
-        const int key = c0 + k * kWThreads + threadIdx.x;
-        if (key < lo || key >= hi)
-            continue;
-        float a = 0.0f;
-        if constexpr (RR != 0) {
+        for (int k = 0; k < kKeys; ++k) {
+            const int key = c0 + k * kWThreads + threadIdx.x;
+            if (key < lo || key >= hi)
+                continue;
+            float a = 0.0f;
 #pragma unroll
             for (int i = 0; i < RR; ++i)
                 a += fast_exp2(v[k][i] - lse2[i]);
-        } else {
-            const float4 *src = reinterpret_cast<const float4 *>(sc + (size_t)key * R);
-            for (int i = 0; i < R; i += 4) {
-                const float4 x = src[i / 4];
-                a += (fast_exp2(x.x - lse2[i]) + fast_exp2(x.y - lse2[i + 1])) +
-                     (fast_exp2(x.z - lse2[i + 2]) + fast_exp2(x.w - lse2[i + 3]));
+            W[key] = w[k] + a;
+        }
+    } else {
+        // `per` lanes (a power of two) share a key, 4 rows each at a time
+        int per = 4;
+        while (per < 32 && per * 4 < R)
+            per *= 2;
+        const int sub = lane % per, kpw = 32 / per;   // keys of a warp at a time
+        const int end = min(hi, c0 + kChunk);
+        constexpr int kU = 4;                         // and their loads in flight
+        for (int k0 = c0 + warp * kpw * kU; k0 < end; k0 += (kWThreads / 32) * kpw * kU) {
+            float a[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                a[u] = 0.0f;
+            for (int i = 4 * sub; i < R; i += 4 * per) {
+                float4 x[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int key = k0 + u * kpw + lane / per;
+                    x[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    if (key >= lo && key < end)
+                        x[u] = *reinterpret_cast<const float4 *>(sc + (size_t)key * R + i);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    a[u] += (fast_exp2(x[u].x - lse2[i]) + fast_exp2(x[u].y - lse2[i + 1])) +
+                            (fast_exp2(x[u].z - lse2[i + 2]) + fast_exp2(x[u].w - lse2[i + 3]));
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int key = k0 + u * kpw + lane / per;
+                for (int o = per / 2; o > 0; o >>= 1)
+                    a[u] += __shfl_xor_sync(0xffffffffu, a[u], o);
+                if (sub == 0 && key >= lo && key < end)
+                    W[key] += a[u];
             }
         }
-        W[key] = w[k] + a;
     }
 }
 
 template <int BS, int RR>
 cudaError_t launch_w(const DecodeParams &p, cudaStream_t stream)
 {
-    const int chunks = (p.score_keys + kChunk - 1) / kChunk;
+    const int chunks = (p.score_keys + kChunkOf<RR> - 1) / kChunkOf<RR>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(chunks + (p.rows + kWThreads / 32 - 1) / (kWThreads / 32)),
                        (unsigned)p.num_kv_heads, (unsigned)p.batch);
