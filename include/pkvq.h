@@ -414,8 +414,8 @@ PKVQ_API pkvq_status pkvq_paged_attn_decode_weights(const pkvq_cache *cache, con
  *   new_context_lens int32 [batch], not the context_lens array
  *   weights_out      nullable fp32 [batch][num_kv_heads][weight_out_stride],
  *                    weight_out_stride >= budget; must not overlap weights
- * num_sink + num_recent must not exceed budget; batch and num_kv_heads at most
- * 65535.  batch == 0 is a no-op.
+ * num_sink + num_recent must not exceed budget (at most 2^30); batch and
+ * num_kv_heads at most 65535.  batch == 0 is a no-op.
  */
 PKVQ_API pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights,
                                    int64_t weight_stride, const int32_t *block_table,

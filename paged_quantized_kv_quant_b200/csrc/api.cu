@@ -590,8 +590,8 @@ pkvq_status pkvq_kv_evict(const pkvq_cache *cache, const float *weights, int64_t
         dst_max_blocks < 0 || (long long)dst_max_blocks * cache->block_size < budget ||
         weight_stride < 0 || (weights_out && weight_out_stride < budget))
         return PKVQ_ERR_INVALID_ARG;
-    if (batch > kMaxGridYZ || cache->num_kv_heads > kMaxGridYZ)
-        return PKVQ_ERR_UNSUPPORTED;   // the launch grid
+    if (batch > kMaxGridYZ || cache->num_kv_heads > kMaxGridYZ || budget > (1 << 30))
+        return PKVQ_ERR_UNSUPPORTED;   // the launch grid; 32-bit positions
     if (batch == 0)
         return PKVQ_OK;
     if (!weights || !block_table || !context_lens || !dst_block_table || !keep_out ||

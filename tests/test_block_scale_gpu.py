@@ -180,6 +180,25 @@ def test_decode(fmt, hq, hkv, bs, ctx, ql, window):
     assert pk.device_status() == 0
 
 
+@pytest.mark.parametrize("fmt,hq,ql,bs", [(pk.KV_INT8_BLOCK, 8, 1, 16), (pk.KV_E4M3_BLOCK, 8, 2, 32),
+                                          (pk.KV_INT8_BLOCK, 16, 5, 16)])
+def test_many_sequences_share_the_splits(fmt, hq, ql, bs):
+    """More than 32 sequences of very different lengths: every key has a split."""
+    r = np.random.default_rng(54)
+    hkv = 2
+    ctx = [int(x) for x in r.choice([0, 1, 15, 16, 17, 200, 700, 1500], 43)]
+    blocks, table, _ = lay_out(ctx, bs, 55)
+    cache = random_cache(fmt, blocks, bs, hkv, 56)
+    host = Host(cache)
+    q = queries(r, len(ctx), ql, hq, D)
+    lse = torch.empty((len(ctx), ql, hq), device="cuda")
+    # (the bound may lie above every length)
+    out = pk.paged_attn_decode(cache, cuda(q), cuda(table), cuda(np.int32(ctx)), table.shape[1] * bs, SCALE, lse=lse)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, c in enumerate(ctx):
+        check_rows(out[b], lse[b], q[b].astype(float), host, table, b, c, c - ql + np.arange(ql), hq)
+
+
 @pytest.mark.parametrize("fmt", BLOCK)
 def test_decode_scale_zero_huge_and_tiny(fmt):
     """Blocks whose V scale is 0 (all codes 0), 2^9 and 2^-33: no overflow, no lost rows."""

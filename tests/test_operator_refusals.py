@@ -118,6 +118,7 @@ def test_evict_refusals(lib):
     for name in ("w", "bt", "ctx", "dst", "keep", "lens"):
         assert evict(lib, c, **{name: None}) == INVALID
     assert evict(lib, c, B=65536) == UNSUPPORTED
+    assert evict(lib, c, budget=(1 << 30) + 1, dstb=(1 << 27), wos=1 << 31) == UNSUPPORTED
     assert evict(lib, cache(block_size=24)) == UNSUPPORTED
     assert evict(lib, c, B=0, w=None) == OK
 
