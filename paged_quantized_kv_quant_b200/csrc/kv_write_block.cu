@@ -17,8 +17,14 @@
 // or 4 warps and one exchange through shared memory), the rows stay in
 // registers between the reduction and the encoding, and each element is read
 // and written once; no atomics.  Consecutive units take consecutive heads, whose
-// rows are adjacent in memory.  Bound by memory: 512 bytes read and 256 written
-// per token and KV head.
+// rows are adjacent in memory.
+//
+// The floor is memory: 512 bytes read and 256 written per token and KV head, 17.5
+// us for 18.4K tokens x 8 heads (E4M3).  Measured 30.9 us, 3.7 TB/s: half the issue
+// slots go to the exact conversion (two bracketing products per element).  One
+// CTA per block took 53 us, one warp for K and V of its rows (half the warps in
+// flight) 39 us; a grid without index divisions and loads without predicates for
+// whole blocks 32.7 us.
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"

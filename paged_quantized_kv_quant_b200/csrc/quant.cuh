@@ -199,8 +199,8 @@ __device__ __forceinline__ uint4 finite8(uint4 x)
 
 // 8 finite fp16 values -> 8 codes of x / s by division, for the rare pieces
 // whose bracketing products disagree.  Not inlined: 16 copies of 8 divisions
-// per thread kept the write kernel waiting for its instructions (58 us instead
-// of 22 us for 18K tokens x 8 heads).
+// per thread kept the write kernel waiting for its instructions (53 us instead
+// of 39 us for 18K tokens x 8 heads, then with one warp for both K and V).
 template <int KVT>
 __device__ __noinline__ uint2 quant_block_divide(uint4 x, float s)
 {
