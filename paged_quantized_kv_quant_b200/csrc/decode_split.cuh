@@ -37,9 +37,11 @@
 // scale folds into the score multiplier of its block; the V scale vs folds
 // into the exponent, p' = 2^(s + log2 vs - M) with M the running maximum of
 // s + log2 vs, so that O += p' code needs no product per element, codes enter
-// the tensor core exactly and p' <= 1 in fp16 whatever the scales; the sum is
-// kept as l += p' / vs in fp32.  A block costs two scalars (loaded 16 blocks
-// ahead into registers) and one multiply-add per row.
+// the tensor core exactly and p' <= 1 in fp16; the sum is kept as l += p' / vs in
+// fp32.  A block's p' loses fp16 bits only where another block's weights times its
+// scale outweigh them, and then its values weigh as little in the output (a block
+// of zeros outweighs nothing: kZeroScaleStandIn).  A block costs two scalars (loaded
+// 16 blocks ahead into registers) and one multiply-add per row.
 // FP16 caches hold the values themselves: a row of 128 values is 256 bytes,
 // fetched as two 128-byte-wide boxes (d 0-63, d 64-127) and read straight
 // into the MMA fragments.
@@ -603,11 +605,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
                 phys = 0;   // recorded when its copy is issued
 #endif
             const size_t si_ = (size_t)phys * p.num_kv_heads + h;
-            const float vs = __ldg(p.v_scale_blk + si_);
+            const float v0 = __ldg(p.v_scale_blk + si_);
+            const float vs = v0 > 0.0f ? v0 : kZeroScaleStandIn;
             kf = kfac * __ldg(p.k_scale_blk + si_);
-            // scale 0: every code of the block is 0, any factor serves
-            lv = vs > 0.0f ? log2f(vs) : 0.0f;
-            iv = vs > 0.0f ? __frcp_rn(vs) : 1.0f;
+            lv = log2f(vs);
+            iv = __frcp_rn(vs);
         }
     };
     if constexpr (kBlk)

@@ -33,6 +33,14 @@ __host__ __device__ constexpr bool kv_has_block_scale(int kvt)
     return kvt == kKvInt8Blk || kvt == kKvE4m3Blk;
 }
 
+// What a V scale of 0 counts as where the scale enters the exponent.  All codes of
+// such a block are 0, so its values add nothing whatever the factor, but its keys'
+// s + log2 vs take part in the running maximum: a factor above the real scales
+// would push the other blocks' fp16 weights down to subnormals or 0 (1 did).  2^-34
+// is below every real scale (at least 2^-24 / 448, 2^-32.8); its log2 and reciprocal
+// are exact.
+constexpr float kZeroScaleStandIn = 0x1p-34f;
+
 struct KvWriteParams {
     uint8_t *k_cache, *v_cache;
     const float *k_scale, *v_scale;        // FP8 formats

@@ -137,14 +137,14 @@ __device__ __forceinline__ float max16(const float *v)
 // as the softmax of the tensor-core kernels takes them: a key's exponent is
 // ks * (q . codes) + lv - M and its weight's sum counts iv times, with ks =
 // |softmax scale| log2(e) times the K scale, lv = log2 and iv = 1 / of the V
-// scale.  ks stays positive, so that a masked score, -inf, remains one: where a
+// scale.  ks stays positive, so that a masked score, -inf, remains one: where the K
 // scale is 0, or the group holds no key, all its codes are 0.
 struct BlockFactors {
     float ks, lv, iv;
     __device__ __forceinline__ BlockFactors(float kfac, float k_scale, float v_scale, bool live)
     {
         ks = live ? fmaxf(fabsf(kfac) * k_scale, 1e-30f) : 1e-30f;
-        const float vs = live && v_scale > 0.0f ? v_scale : 1.0f;
+        const float vs = live && v_scale > 0.0f ? v_scale : kZeroScaleStandIn;
         lv = log2f(vs);
         iv = __frcp_rn(vs);
     }
