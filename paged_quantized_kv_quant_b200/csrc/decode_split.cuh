@@ -605,9 +605,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
                 phys = 0;   // recorded when its copy is issued
 #endif
             const size_t si_ = (size_t)phys * p.num_kv_heads + h;
-            const float v0 = __ldg(p.v_scale_blk + si_);
+            // (ordinary loads: an appending call's write kernel may still store scales
+            // while this grid is resident, which the read-only path does not allow)
+            const float v0 = p.v_scale_blk[si_];
             const float vs = v0 > 0.0f ? v0 : kZeroScaleStandIn;
-            kf = kfac * __ldg(p.k_scale_blk + si_);
+            kf = kfac * p.k_scale_blk[si_];
             lv = log2f(vs);
             iv = __frcp_rn(vs);
         }
