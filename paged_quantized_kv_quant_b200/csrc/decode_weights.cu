@@ -44,6 +44,9 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
     const SplitInfo si = find_split<BS>(p, -1, b);
     // the split kernel's partial states and scores
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // After a wait that gave up (there or in an earlier call) they are not all there:
+    // the accumulator, which outlives this call, then stays as it was.
+    const bool failed = device_wait_failed(p.status);
 
     if ((int)blockIdx.x >= chunks) {
         const int rr = ((int)blockIdx.x - chunks) * (kWThreads / 32) + warp;
@@ -140,7 +143,8 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
         if (sub == 0 && r < R)
             lse2[r] = L > 0.0f ? M + log2f(L) : INFINITY;
     }
-    __syncthreads();
+    if (__syncthreads_or(failed))
+        return;
     if constexpr (RR != 0) {
 #pragma unroll
         for (int k = 0; k < kKeys; ++k) {
