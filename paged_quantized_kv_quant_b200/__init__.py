@@ -22,7 +22,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import operator
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -320,6 +319,8 @@ class PagedKVCache:
     k_scale_blk: Optional[torch.Tensor] = None
     v_scale_blk: Optional[torch.Tensor] = None
 
+    __slots__ = ("__dict__", "__weakref__", "_kept")
+
     @staticmethod
     def allocate(dtype: int, num_blocks: int, block_size: int, num_kv_heads: int,
                  head_dim: int = 128, device="cuda", k_scale=None, v_scale=None,
@@ -365,21 +366,31 @@ class PagedKVCache:
         return self.k_cache.shape[3] // elem_bytes(self.dtype)
 
     def struct(self, device_ok: bool = False) -> CacheStruct:
-        """The cache as the C ABI sees it.  Kept with the object: the tensors are
-        checked again when one of them, or its address, has changed."""
-        tensors = (self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.k_scale_tok,
-                   self.v_scale_tok, self.k_scale_blk, self.v_scale_blk)
-        seen = [None if t is None else t.data_ptr() for t in tensors]
-        kept = self.__dict__.get("_kept")
-        if kept is not None and not device_ok:
-            old, addresses, dtype, per_layer, cs = kept
-            if (addresses == seen and dtype == self.dtype and per_layer == self.scale_per_layer
-                    and all(map(operator.is_, old, tensors))):
-                return cs
-        cs = self._struct(device_ok)
-        if not device_ok:
-            self.__dict__["_kept"] = (tensors, seen, self.dtype, self.scale_per_layer, cs)
-        return cs
+        """The cache as the C ABI sees it, checked now (the caller's own copy)."""
+        if device_ok:
+            return self._struct(True)
+        return CacheStruct.from_buffer_copy(self._c())
+
+    def _c(self) -> CacheStruct:
+        """The C struct of a call.  Kept with the object, without its tensors: they
+        are checked again when one has another address, shape, layout or type."""
+        try:
+            key = [self.dtype, self.scale_per_layer]
+            for t in (self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.k_scale_tok,
+                      self.v_scale_tok, self.k_scale_blk, self.v_scale_blk):
+                if t is None:
+                    key.append(None)
+                else:
+                    key += (t.data_ptr(), t.shape, t.dtype, t.is_contiguous())
+        except AttributeError:   # not a tensor
+            return self._struct(False)
+        kept = getattr(self, "_kept", None)
+        if kept is None or kept[0] != key:
+            self._kept = kept = (key, self._struct(False))
+        return kept[1]
+
+    def __getstate__(self):   # copies and pickles hold the fields alone
+        return dict(self.__dict__)
 
     def _struct(self, device_ok: bool) -> CacheStruct:
         for name in ("k_cache", "v_cache"):
@@ -424,7 +435,7 @@ def kv_write_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
     _need(k, torch.float16, "k", 3)
     _need(v, torch.float16, "v", 3)
     _need(slot_mapping, torch.int32, "slot_mapping", 1)
-    cs = cache.struct()
+    cs = cache._c()
     _check(_lib().pkvq_kv_write_quant(ctypes.byref(cs), _ptr(k), _ptr(v), _ptr(slot_mapping),
                                       int(slot_mapping.shape[0]), _stream(stream)),
            "kv_write_quant")
@@ -437,7 +448,7 @@ def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
     every sequence b (packed), into a block-scaled cache; context_lens counts
     them.  A block's scale covers the tokens written to it: it grows when a
     louder token arrives, and the block's older codes are rounded again."""
-    cs = cache.struct()
+    cs = cache._c()
     dev = cache.k_cache.get_device()
     B, cols = _rows("context_lens", context_lens), _cols("block_table", block_table)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -454,7 +465,7 @@ def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
 
 def decode_workspace_bytes(cache: PagedKVCache, batch: int, q_len: int, num_q_heads: int,
                            max_context_len: int) -> int:
-    cs = cache.struct()
+    cs = cache._c()
     return int(_lib().pkvq_decode_workspace_bytes(batch, q_len, num_q_heads, max_context_len,
                                                   ctypes.byref(cs)))
 
@@ -482,7 +493,7 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
     """q fp16 [B][q_len][Hq][D] -> out fp16 [B][q_len][Hq][D] (lse fp32 [B][q_len][Hq]).
     sliding_window > 0 limits every query to its last `sliding_window` keys;
     query_pos (int32 [B][q_len]) gives each query's position among the keys."""
-    cs = cache.struct()
+    cs = cache._c()
     dev = cache.k_cache.get_device()
     B, q_len, Hq, shape = _queries(q, cs)
     cols = _cols("block_table", block_table)
@@ -490,7 +501,8 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
         if out is None:
             out = torch.empty_like(q)
         if workspace is None and B:   # contents need not be initialised
-            need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len)
+            need = _lib().pkvq_decode_workspace_bytes(B, q_len, Hq, max_context_len,
+                                                      ctypes.byref(cs))
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
         ws, wbytes = _scratch(workspace, dev)
         _arg("query_pos", query_pos, torch.int32, (B, q_len), dev)
@@ -509,7 +521,7 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
 
 def decode_weights_workspace_bytes(cache: PagedKVCache, batch: int, q_len: int,
                                    num_q_heads: int, max_context_len: int) -> int:
-    cs = cache.struct()
+    cs = cache._c()
     with _on(cache.k_cache):
         return int(_lib().pkvq_decode_weights_workspace_bytes(
             batch, q_len, num_q_heads, max_context_len, ctypes.byref(cs)))
@@ -526,7 +538,7 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
     """paged_attn_decode that also adds every key's softmax weight, summed over
     the query rows of its KV head, to weights fp32 [B][Hkv][>= max_context_len]
     (zero the entries of new tokens).  Input of kv_evict."""
-    cs = cache.struct()
+    cs = cache._c()
     dev = cache.k_cache.get_device()
     B, q_len, Hq, shape = _queries(q, cs)
     cols = _cols("block_table", block_table)
@@ -537,7 +549,8 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
         if out is None:
             out = torch.empty_like(q)
         if workspace is None and B:   # contents need not be initialised
-            need = decode_weights_workspace_bytes(cache, B, q_len, Hq, max_context_len)
+            need = _lib().pkvq_decode_weights_workspace_bytes(B, q_len, Hq, max_context_len,
+                                                              ctypes.byref(cs))
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         ws, wbytes = _scratch(workspace, dev)
         _arg("query_pos", query_pos, torch.int32, (B, q_len), dev)
@@ -566,7 +579,7 @@ def kv_evict(cache: PagedKVCache, weights: torch.Tensor, block_table: torch.Tens
     (distinct blocks that hold no token of these sequences).
     Returns (new_context_lens int32 [B], weights_out fp32 [B][Hkv][W'], keep
     int32 [B][Hkv][budget]: the kept positions, -1 behind the last)."""
-    cs = cache.struct()
+    cs = cache._c()
     dev = cache.k_cache.get_device()
     B, H, budget = _rows("context_lens", context_lens), cs.num_kv_heads, int(budget)
     cols, dst_cols = _cols("block_table", block_table), _cols("dst_block_table", dst_block_table)
@@ -608,7 +621,7 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
     are the keys and values of each sequence's last q_len positions; they are
     quantised into the cache (as kv_write_quant) and attention runs as
     paged_attn_decode."""
-    cs = cache.struct()
+    cs = cache._c()
     dev = cache.k_cache.get_device()
     B, q_len, Hq, shape = _queries(q, cs)
     cols = _cols("block_table", block_table)
@@ -617,7 +630,8 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
         if out is None:
             out = torch.empty_like(q)
         if workspace is None and B:   # contents need not be initialised
-            need = decode_workspace_bytes(cache, B, q_len, Hq, max_context_len)
+            need = _lib().pkvq_decode_workspace_bytes(B, q_len, Hq, max_context_len,
+                                                      ctypes.byref(cs))
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
         ws, wbytes = _scratch(workspace, dev)
         opts = _opts(sliding_window, None)
@@ -640,7 +654,7 @@ def paged_attn_prefill(cache: PagedKVCache, q: torch.Tensor, cu_seqlens_q: torch
                        lse: Optional[torch.Tensor] = None, stream=None,
                        sliding_window: int = 0) -> torch.Tensor:
     """q fp16 [total_q][Hq][D] (packed varlen) -> out fp16 [total_q][Hq][D]."""
-    cs = cache.struct()
+    cs = cache._c()
     dev = cache.k_cache.get_device()
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != cs.head_dim:
         raise ValueError(f"q must be [total_q][num_q_heads][{cs.head_dim}]")
