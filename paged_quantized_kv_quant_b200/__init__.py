@@ -17,11 +17,16 @@ Entry points (same names as the C ABI, without the ``pkvq_`` prefix):
   weights), paged_attn_prefill (sliding_window), merge_attn_states,
   kv_copy_blocks, device_status, status_string, version.  ``dcp`` adds the all-gather step
   of sequence-sharded decode (torch.distributed plumbing).
+
+The paged calls take the batch from q (decode) or context_lens (the others).  Block
+tables, context lengths and cu_seqlens may be longer than the batch needs, and out and
+lse larger than the results, which are written from their start.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -240,6 +245,10 @@ def _on(t: torch.Tensor, stream=None):
     """Context in which `t`'s device and the call's stream are the current ones:
     launches go there, and what the call allocates belongs to that stream."""
     if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):   # anything with a raw cuda_stream
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=t.device)
+        elif stream.device_index != t.get_device():
+            raise ValueError(f"stream must be on the tensors' device, {t.device}")
         return torch.cuda.stream(stream)
     if t.get_device() == torch._C._cuda_getDevice():
         return _SAME_DEVICE
@@ -260,6 +269,25 @@ def _arg(name: str, t, dtype, shape: tuple, device: int) -> Optional[int]:
     _need(t, dtype, name)
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{device}")
+
+
+def _room(name: str, t, dtype, shape: tuple, device: int) -> Optional[int]:
+    """As _arg, for a buffer that may be larger: as many dimensions, and at least
+    as many elements, which the call uses from its start (preallocated tables,
+    lengths and results for more sequences than the call has)."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+                and (t.shape == shape
+                     or (t.dim() == len(shape) and t.numel() >= math.prod(shape)))):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name)
+    if t.dim() != len(shape) or t.numel() < math.prod(shape):
+        raise ValueError(f"{name} must hold {shape}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be on cuda:{device}")
 
 
@@ -455,8 +483,8 @@ def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
         raise ValueError("k must be [tokens][num_kv_heads][head_dim]")
     rows = (k.shape[0], cs.num_kv_heads, cs.head_dim)
     args = (_arg("k", k, torch.float16, rows, dev), _arg("v", v, torch.float16, rows, dev), rows[0],
-            _arg("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev),
-            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _room("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev),
+            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
             _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_new_len))
     with _on(k, stream):
         _check(_lib().pkvq_kv_write_block_quant(ctypes.byref(cs), *args, _stream(stream, dev)),
@@ -509,10 +537,10 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
         opts = _opts(sliding_window, query_pos)
         _check(_lib().pkvq_paged_attn_decode_ex(
             ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
-            _arg("out", out, torch.float16, shape, dev),
-            _arg("lse", lse, torch.float32, shape[:3], dev),
-            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            _room("out", out, torch.float16, shape, dev),
+            _room("lse", lse, torch.float32, shape[:3], dev),
+            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _room("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
             None if opts is None else ctypes.byref(opts), ws, wbytes, _stream(stream, dev)),
             "paged_attn_decode")
@@ -557,10 +585,10 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
         opts = _opts(sliding_window, query_pos)
         _check(_lib().pkvq_paged_attn_decode_weights(
             ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
-            _arg("out", out, torch.float16, shape, dev),
-            _arg("lse", lse, torch.float32, shape[:3], dev),
-            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            _room("out", out, torch.float16, shape, dev),
+            _room("lse", lse, torch.float32, shape[:3], dev),
+            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _room("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
             None if opts is None else ctypes.byref(opts),
             _arg("weights", weights, torch.float32, (B, cs.num_kv_heads, W), dev), W, ws, wbytes,
@@ -599,10 +627,10 @@ def kv_evict(cache: PagedKVCache, weights: torch.Tensor, block_table: torch.Tens
         w_out = weights_out.shape[-1]
         _check(_lib().pkvq_kv_evict(
             ctypes.byref(cs), _arg("weights", weights, torch.float32, (B, H, W), dev), W,
-            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
             _arg("context_lens", context_lens, torch.int32, (B,), dev), B, budget,
             int(num_sink), int(num_recent),
-            _arg("dst_block_table", dst_block_table, torch.int32, (B, dst_cols), dev), dst_cols,
+            _room("dst_block_table", dst_block_table, torch.int32, (B, dst_cols), dev), dst_cols,
             _arg("keep", keep, torch.int32, (B, H, budget), dev),
             _arg("new_context_lens", new_context_lens, torch.int32, (B,), dev),
             _arg("weights_out", weights_out, torch.float32, (B, H, w_out), dev), w_out,
@@ -638,10 +666,10 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
         _check(_lib().pkvq_paged_attn_decode_append(
             ctypes.byref(cs), _arg("k_new", k_new, torch.float16, new, dev),
             _arg("v_new", v_new, torch.float16, new, dev),
-            _arg("q", q, torch.float16, shape, dev), _arg("out", out, torch.float16, shape, dev),
-            _arg("lse", lse, torch.float32, shape[:3], dev),
-            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            _arg("q", q, torch.float16, shape, dev), _room("out", out, torch.float16, shape, dev),
+            _room("lse", lse, torch.float32, shape[:3], dev),
+            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _room("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
             None if opts is None else ctypes.byref(opts), ws, wbytes, _stream(stream, dev)),
             "paged_attn_decode_append")
@@ -666,10 +694,10 @@ def paged_attn_prefill(cache: PagedKVCache, q: torch.Tensor, cu_seqlens_q: torch
         opts = _opts(sliding_window, None)
         _check(_lib().pkvq_paged_attn_prefill_ex(
             ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
-            _arg("out", out, torch.float16, shape, dev),
-            _arg("lse", lse, torch.float32, shape[:2], dev),
-            _arg("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev),
-            _arg("block_table", block_table, torch.int32, (B, cols), dev), cols,
+            _room("out", out, torch.float16, shape, dev),
+            _room("lse", lse, torch.float32, shape[:2], dev),
+            _room("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev),
+            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
             _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_q_len),
             shape[1], float(softmax_scale), None if opts is None else ctypes.byref(opts), None,
             0, _stream(stream, dev)), "paged_attn_prefill")
