@@ -46,7 +46,9 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // After a wait that gave up (there or in an earlier call) they are not all there:
     // the accumulator, which outlives this call, then stays as it was.
-    const bool failed = device_wait_failed(p.status);
+    __shared__ bool failed;
+    if (threadIdx.x == 0)
+        failed = device_wait_failed(p.status);
 
     if ((int)blockIdx.x >= chunks) {
         const int rr = ((int)blockIdx.x - chunks) * (kWThreads / 32) + warp;
@@ -143,7 +145,8 @@ decode_weights_kernel(const DecodeParams p, const int chunks)
         if (sub == 0 && r < R)
             lse2[r] = L > 0.0f ? M + log2f(L) : INFINITY;
     }
-    if (__syncthreads_or(failed))
+    __syncthreads();
+    if (failed)
         return;
     if constexpr (RR != 0) {
 #pragma unroll

@@ -311,14 +311,16 @@ __global__ void __launch_bounds__(BS * 8) evict_move_kernel(const EvictParams p)
     __shared__ float sk[BS], sv[BS];
     const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int m = min(evict_tokens(p, b), p.budget);
-    const bool some = i * BS < m;
-    const int dst = some ? __ldg(p.dst_block_table + (size_t)b * p.dst_max_blocks + i) : 0;
-    // The list of kept positions comes from the kernel before.  CTAs without rows
-    // wait too: in a call whose sequences are all empty nobody else would, and this
-    // grid, which stands for the call in its stream, could end before that kernel.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!some)
+    if (i * BS >= m) {
+        // (wait all the same: in a call whose sequences are all empty nobody else
+        // would, and this grid, which stands for the call in its stream, could end
+        // before the kernel it depends on)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
+    }
+    const int dst = __ldg(p.dst_block_table + (size_t)b * p.dst_max_blocks + i);
+    // the list of kept positions comes from the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 #ifdef PKVQ_BOUNDS_CHECK
     if (dst < 0 || dst >= p.num_blocks) {
         if (threadIdx.x == 0)
