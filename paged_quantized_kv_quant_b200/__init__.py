@@ -291,18 +291,31 @@ def _room(name: str, t, dtype, shape: tuple, device: int) -> Optional[int]:
     raise ValueError(f"{name} must be on cuda:{device}")
 
 
-def _cols(name: str, t) -> int:
-    """Columns of a 2-D tensor."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
-    return t.shape[1]
+def _table(name: str, t, rows: int, device: int):
+    """(address, columns) of a block table of at least `rows` rows."""
+    try:
+        shape = t.shape
+        if (len(shape) == 2 and shape[0] >= rows and t.dtype is torch.int32
+                and t.get_device() == device and t.is_contiguous()):
+            return t.data_ptr(), shape[1]
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < rows:
+        raise ValueError(f"{name} must be a 2-D tensor of at least {rows} rows")
+    return _arg(name, t, torch.int32, tuple(t.shape), device), t.shape[1]
 
 
-def _rows(name: str, t) -> int:
-    """Entries of a 1-D tensor."""
+def _lens(name: str, t, device: int):
+    """(address, entries) of an int32 vector whose length is the batch."""
+    try:
+        if (t.dtype is torch.int32 and t.dim() == 1 and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise ValueError(f"{name} must be a 1-D tensor")
-    return t.shape[0]
+    return _arg(name, t, torch.int32, tuple(t.shape), device), t.numel()
 
 
 def _scratch(workspace: Optional[torch.Tensor], device: int):
@@ -403,13 +416,11 @@ class PagedKVCache:
         """The C struct of a call.  Kept with the object, without its tensors: they
         are checked again when one has another address, shape, layout or type."""
         try:
-            key = [self.dtype, self.scale_per_layer]
-            for t in (self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.k_scale_tok,
-                      self.v_scale_tok, self.k_scale_blk, self.v_scale_blk):
-                if t is None:
-                    key.append(None)
-                else:
-                    key += (t.data_ptr(), t.shape, t.dtype, t.is_contiguous())
+            key = [None if t is None else (t.data_ptr(), t.shape, t.dtype, t.is_contiguous())
+                   for t in (self.k_cache, self.v_cache, self.k_scale, self.v_scale,
+                             self.k_scale_tok, self.v_scale_tok, self.k_scale_blk,
+                             self.v_scale_blk)]
+            key += (self.dtype, self.scale_per_layer)
         except AttributeError:   # not a tensor
             return self._struct(False)
         kept = getattr(self, "_kept", None)
@@ -478,14 +489,14 @@ def kv_write_block_quant(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor,
     louder token arrives, and the block's older codes are rounded again."""
     cs = cache._c()
     dev = cache.k_cache.get_device()
-    B, cols = _rows("context_lens", context_lens), _cols("block_table", block_table)
+    lens, B = _lens("context_lens", context_lens, dev)
+    table, cols = _table("block_table", block_table, B, dev)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [tokens][num_kv_heads][head_dim]")
     rows = (k.shape[0], cs.num_kv_heads, cs.head_dim)
     args = (_arg("k", k, torch.float16, rows, dev), _arg("v", v, torch.float16, rows, dev), rows[0],
             _room("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev),
-            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_new_len))
+            table, cols, lens, B, int(max_new_len))
     with _on(k, stream):
         _check(_lib().pkvq_kv_write_block_quant(ctypes.byref(cs), *args, _stream(stream, dev)),
                "kv_write_block_quant")
@@ -504,12 +515,17 @@ def _opts(sliding_window: int, query_pos: Optional[torch.Tensor]):
     return AttnOpts(int(sliding_window), None if query_pos is None else query_pos.data_ptr())
 
 
-def _queries(q: torch.Tensor, cs: CacheStruct):
-    """(batch, q_len, query heads, shape) of decode queries for a cache."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != cs.head_dim:
+def _queries(q: torch.Tensor, cs: CacheStruct, device: int):
+    """(address, batch, q_len, query heads, shape) of decode queries for a cache."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError(f"q must be [batch][q_len][num_q_heads][{cs.head_dim}]")
     shape = tuple(q.shape)
-    return shape[0], shape[1], shape[2], shape
+    B, q_len, Hq, D = shape
+    if D != cs.head_dim:
+        raise ValueError(f"q must be [batch][q_len][num_q_heads][{cs.head_dim}]")
+    if q.dtype is torch.float16 and q.get_device() == device and q.is_contiguous():
+        return q.data_ptr(), B, q_len, Hq, shape
+    return _arg("q", q, torch.float16, shape, device), B, q_len, Hq, shape
 
 
 def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Tensor,
@@ -523,8 +539,8 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
     query_pos (int32 [B][q_len]) gives each query's position among the keys."""
     cs = cache._c()
     dev = cache.k_cache.get_device()
-    B, q_len, Hq, shape = _queries(q, cs)
-    cols = _cols("block_table", block_table)
+    q_ptr, B, q_len, Hq, shape = _queries(q, cs, dev)
+    table, cols = _table("block_table", block_table, B, dev)
     with _on(q, stream):
         if out is None:
             out = torch.empty_like(q)
@@ -536,11 +552,10 @@ def paged_attn_decode(cache: PagedKVCache, q: torch.Tensor, block_table: torch.T
         _arg("query_pos", query_pos, torch.int32, (B, q_len), dev)
         opts = _opts(sliding_window, query_pos)
         _check(_lib().pkvq_paged_attn_decode_ex(
-            ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
-            _room("out", out, torch.float16, shape, dev),
+            ctypes.byref(cs), q_ptr, _room("out", out, torch.float16, shape, dev),
             _room("lse", lse, torch.float32, shape[:3], dev),
-            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _room("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            table, cols, _room("context_lens", context_lens, torch.int32, (B,), dev),
+            B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
             None if opts is None else ctypes.byref(opts), ws, wbytes, _stream(stream, dev)),
             "paged_attn_decode")
@@ -568,8 +583,8 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
     (zero the entries of new tokens).  Input of kv_evict."""
     cs = cache._c()
     dev = cache.k_cache.get_device()
-    B, q_len, Hq, shape = _queries(q, cs)
-    cols = _cols("block_table", block_table)
+    q_ptr, B, q_len, Hq, shape = _queries(q, cs, dev)
+    table, cols = _table("block_table", block_table, B, dev)
     if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
         raise ValueError("weights must be [batch][num_kv_heads][positions]")
     W = weights.shape[2]
@@ -584,11 +599,10 @@ def paged_attn_decode_weights(cache: PagedKVCache, q: torch.Tensor, block_table:
         _arg("query_pos", query_pos, torch.int32, (B, q_len), dev)
         opts = _opts(sliding_window, query_pos)
         _check(_lib().pkvq_paged_attn_decode_weights(
-            ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
-            _room("out", out, torch.float16, shape, dev),
+            ctypes.byref(cs), q_ptr, _room("out", out, torch.float16, shape, dev),
             _room("lse", lse, torch.float32, shape[:3], dev),
-            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _room("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            table, cols, _room("context_lens", context_lens, torch.int32, (B,), dev),
+            B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
             None if opts is None else ctypes.byref(opts),
             _arg("weights", weights, torch.float32, (B, cs.num_kv_heads, W), dev), W, ws, wbytes,
@@ -609,8 +623,10 @@ def kv_evict(cache: PagedKVCache, weights: torch.Tensor, block_table: torch.Tens
     int32 [B][Hkv][budget]: the kept positions, -1 behind the last)."""
     cs = cache._c()
     dev = cache.k_cache.get_device()
-    B, H, budget = _rows("context_lens", context_lens), cs.num_kv_heads, int(budget)
-    cols, dst_cols = _cols("block_table", block_table), _cols("dst_block_table", dst_block_table)
+    lens, B = _lens("context_lens", context_lens, dev)
+    H, budget = cs.num_kv_heads, int(budget)
+    table, cols = _table("block_table", block_table, B, dev)
+    dst_table, dst_cols = _table("dst_block_table", dst_block_table, B, dev)
     if budget < 1:
         raise ValueError("budget must be at least 1")
     if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
@@ -627,10 +643,9 @@ def kv_evict(cache: PagedKVCache, weights: torch.Tensor, block_table: torch.Tens
         w_out = weights_out.shape[-1]
         _check(_lib().pkvq_kv_evict(
             ctypes.byref(cs), _arg("weights", weights, torch.float32, (B, H, W), dev), W,
-            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, budget,
+            table, cols, lens, B, budget,
             int(num_sink), int(num_recent),
-            _room("dst_block_table", dst_block_table, torch.int32, (B, dst_cols), dev), dst_cols,
+            dst_table, dst_cols,
             _arg("keep", keep, torch.int32, (B, H, budget), dev),
             _arg("new_context_lens", new_context_lens, torch.int32, (B,), dev),
             _arg("weights_out", weights_out, torch.float32, (B, H, w_out), dev), w_out,
@@ -651,8 +666,8 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
     paged_attn_decode."""
     cs = cache._c()
     dev = cache.k_cache.get_device()
-    B, q_len, Hq, shape = _queries(q, cs)
-    cols = _cols("block_table", block_table)
+    q_ptr, B, q_len, Hq, shape = _queries(q, cs, dev)
+    table, cols = _table("block_table", block_table, B, dev)
     new = (B, q_len, cs.num_kv_heads, cs.head_dim)
     with _on(q, stream):
         if out is None:
@@ -666,10 +681,10 @@ def paged_attn_decode_append(cache: PagedKVCache, k_new: torch.Tensor, v_new: to
         _check(_lib().pkvq_paged_attn_decode_append(
             ctypes.byref(cs), _arg("k_new", k_new, torch.float16, new, dev),
             _arg("v_new", v_new, torch.float16, new, dev),
-            _arg("q", q, torch.float16, shape, dev), _room("out", out, torch.float16, shape, dev),
+            q_ptr, _room("out", out, torch.float16, shape, dev),
             _room("lse", lse, torch.float32, shape[:3], dev),
-            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _room("context_lens", context_lens, torch.int32, (B,), dev), B, q_len, Hq,
+            table, cols, _room("context_lens", context_lens, torch.int32, (B,), dev),
+            B, q_len, Hq,
             int(max_context_len), float(softmax_scale),
             None if opts is None else ctypes.byref(opts), ws, wbytes, _stream(stream, dev)),
             "paged_attn_decode_append")
@@ -687,18 +702,18 @@ def paged_attn_prefill(cache: PagedKVCache, q: torch.Tensor, cu_seqlens_q: torch
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != cs.head_dim:
         raise ValueError(f"q must be [total_q][num_q_heads][{cs.head_dim}]")
     shape = tuple(q.shape)
-    B, cols = _rows("context_lens", context_lens), _cols("block_table", block_table)
+    q_ptr = _arg("q", q, torch.float16, shape, dev)
+    lens, B = _lens("context_lens", context_lens, dev)
+    table, cols = _table("block_table", block_table, B, dev)
     with _on(q, stream):
         if out is None:
             out = torch.empty_like(q)
         opts = _opts(sliding_window, None)
         _check(_lib().pkvq_paged_attn_prefill_ex(
-            ctypes.byref(cs), _arg("q", q, torch.float16, shape, dev),
-            _room("out", out, torch.float16, shape, dev),
+            ctypes.byref(cs), q_ptr, _room("out", out, torch.float16, shape, dev),
             _room("lse", lse, torch.float32, shape[:2], dev),
             _room("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev),
-            _room("block_table", block_table, torch.int32, (B, cols), dev), cols,
-            _arg("context_lens", context_lens, torch.int32, (B,), dev), B, int(max_q_len),
+            table, cols, lens, B, int(max_q_len),
             shape[1], float(softmax_scale), None if opts is None else ctypes.byref(opts), None,
             0, _stream(stream, dev)), "paged_attn_prefill")
     return out
