@@ -39,12 +39,14 @@ struct BlockWindow {
     const int32_t *row;
     int n, wbase, w0, w1;
 
-    __device__ __forceinline__ void init(const int32_t *r, int nread, int lane)
+    // Entries below `first` (< 32), which nobody sees, stand for entry `first`.
+    __device__ __forceinline__ void init(const int32_t *r, int nread, int lane, int first = 0)
     {
         row = r;
         n = nread;
         wbase = 0;
-        w0 = lane < n ? __ldg(r + lane) : 0;
+        const int e = max(lane, first);
+        w0 = e < n ? __ldg(r + e) : 0;
         w1 = 32 + lane < n ? __ldg(r + 32 + lane) : 0;
     }
 

@@ -211,9 +211,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         return;
     const int ctx = p.context_lens[b];
     const int G = p.group;
-    // first key tile any row of the CTA sees (tile A holds the lower positions)
-    const int jbase =
-        p.window > 0 ? max(0, ctx - q_len + 2 * pair * p.tokens_per_tile - p.window + 1) / kKT : 0;
+    // first key and key tile any row of the CTA sees (tile A holds the lower positions)
+    const int first_key =
+        p.window > 0 ? max(0, ctx - q_len + 2 * pair * p.tokens_per_tile - p.window + 1) : 0;
+    const int jbase = first_key / kKT;
     const QTile qt[2] = {make_qtile(2 * pair, p.tokens_per_tile, q_len, ctx, jbase),
                          make_qtile(2 * pair + 1, p.tokens_per_tile, q_len, ctx, jbase)};
     const int ntiles = max(qt[0].ntiles, qt[1].ntiles);   // counted from jbase
@@ -263,10 +264,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                            p.num_blocks, p.status, p.k_scale_blk, p.v_scale_blk};
         BlockWindow w;
         // every index stays inside the table row, even for a context longer
-        // than the row can address (a caller error: those keys read block 0)
+        // than the row can address (a caller error: those keys read block 0).
+        // Blocks of the first tile that lie below every row's window may be gone:
+        // their (masked) rows come from the window's first block.
         w.init(p.block_table + (size_t)b * p.max_blocks_per_seq + blk_base,
                min(min(nblk_seq - blk_base, ntiles * kBPT), p.max_blocks_per_seq - blk_base),
-               lane);
+               lane, first_key / BS - blk_base);
         // FP16: each tile goes straight into K/V buffer j % kKVBufs
         constexpr int kRing = KVT == kKvFp16 ? kKVBufs : kCodeStages;
         int pf_next = kRing;
