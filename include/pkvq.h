@@ -356,7 +356,11 @@ PKVQ_API pkvq_status pkvq_prompt_attn(const pkvq_prompt *t, void *out, float *ls
                                    float softmax_scale, int32_t sliding_window, void *stream);
 
 /* Workspace bytes of pkvq_paged_attn_decode_weights (0 on invalid arguments):
- * the split-KV partial states and the fp32 score of every (query row, key). */
+ * the split-KV partial states and the fp32 score of every (query row, key):
+ * 4 * batch * num_kv_heads * r * max_context_len bytes (rounded up to whole
+ * blocks) with r = q_len * group query rows per KV head, rounded up to a multiple
+ * of 4 above 2.  8 sequences of 128K with 4 KV heads take 134 MB at 8 rows and
+ * 0.67 GB at 40, for each call in flight; a smaller max_context_len takes less. */
 PKVQ_API size_t pkvq_decode_weights_workspace_bytes(int32_t batch, int32_t q_len,
                                    int32_t num_q_heads, int32_t max_context_len,
                                    const pkvq_cache *cache);

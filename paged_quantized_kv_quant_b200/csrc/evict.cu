@@ -16,10 +16,11 @@
 // min(equal before, ties).  A cluster of up to 8 CTAs shares a row: each keeps
 // its slice's keys in shared memory (one read of the weights), counts into its
 // own histogram (four copies by lane: neighbours' weights share digits) and adds
-// the non-zero counts to every CTA's totals over distributed shared memory.  The
-// passes' latency, not bytes, bounds it: about 1.8 us each, of which the cluster
-// barrier takes 0.7 (32 rows of 32K: 17.6 us in all; with 8,192 positions per CTA
-// 18.5 us).  Measured and not kept: one CTA for a row of 32K (38 us);
+// the non-zero counts to every CTA's totals over distributed shared memory.  Its
+// time goes to the passes one after the other, not to bytes: about 1.8 us each, of
+// which the cluster barrier takes 0.7 (32 rows of 32K: 17.6 us in all; with 8,192
+// positions per CTA 18.5 us); each pass walks the whole slice, although after the
+// first digit few keys still matter.  Measured and not kept: one CTA for a row of 32K (38 us);
 // 11-bit digits, in two or three passes (reading 8 x 8 KB of other CTAs'
 // histograms: 28.6 us; adding the non-zero counts: a microsecond more than this).
 //

@@ -128,8 +128,9 @@ struct DecodePlan {
     int score_keys, score_rows;
 };
 
-// Split plan for a decode shape on the current device (kv_dtype: kKvFp8 or
-// kKvInt8, whose kernels differ in registers and so in occupancy).
+// Split plan for a decode shape on the current device (kv_dtype: any format; their
+// kernels differ in registers and so in occupancy, and block-scaled formats take
+// finer splits and the left-over slots).
 bool decode_plan(int kv_dtype, int batch, int q_len, int num_q_heads, int num_kv_heads,
                  int block_size, int max_context_len, bool weights, DecodePlan *plan);
 

@@ -20,9 +20,10 @@
 // rows are adjacent in memory.
 //
 // The floor is memory: 512 bytes read and 256 written per token and KV head, 17.5
-// us for 18.4K tokens x 8 heads (E4M3).  Measured 30.9 us, 3.7 TB/s: 57 % of the
-// issue slots are taken, most by the exact conversion (two bracketing products
-// per element).  With the division inlined, one CTA per block and one warp for K
+// us for 18.4K tokens x 8 heads (E4M3).  Measured 30.9 us, 3.7 TB/s, so no unit is
+// at its limit: 67 % of the issue slots are taken, most by the exact conversion
+// (two bracketing products and two conversions per element), and 64 registers leave
+// half of the SM's warps to hide the loads.  With the division inlined, one CTA per block and one warp for K
 // and V of 16 rows both took 53 us; that warp with the division out of line 39 us,
 // a warp each for K and V (this form) 31 us.  Not kept: a grid without index
 // divisions, 32.7 us.
